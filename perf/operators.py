@@ -262,13 +262,12 @@ def _run_own(c):
     import hybrid_attention_ssm_head_b200 as hy
     stream = torch.cuda.current_stream()
     if c["op"] == "heads":
-        if "call" not in c:  # the views and the rotation that a program fills in once for its buffers
-            opt = ROPE[c["scaling"]]
-            c["call"] = (hy.make_head_rows(c["q"], c["q_out"], c["wq"]), hy.make_head_rows(c["k"], c["k_out"], c["wk"]),
-                         hy.make_rope(c["rot"], c["layout"], scaling=c["scaling"], **opt))
-        q, k, rope = c["call"]
-        hy.hymba_qk_norm_rope(c["dtype"], c["batch"], c["rows"], c["dim"], q, k, c["norm"], 1e-6, rope, c["pos0"],
-                              c["positions"], stream)
+        if "call" not in c:  # the description of its buffers and of the rotation that a program fills in once
+            rope = hy.make_rope(c["rot"], c["layout"], scaling=c["scaling"], **ROPE[c["scaling"]])
+            c["call"] = hy.make_qk_norm_rope(c["q"], c["k"], c["q_out"], c["k_out"], norm=c["norm"], eps=1e-6,
+                                             q_weight=c["wq"], k_weight=c["wk"], rope=rope, pos0=c["pos0"],
+                                             positions=c["positions"])
+        hy.hymba_qk_norm_rope(c["call"], stream)
         return c["q_out"], c["k_out"]
     if "call" not in c:  # the description of its buffers and the workspace that a program keeps
         args = hy.make_linear_attention(c["q"], c["k"], c["v"], c["o"], c["g"], in_scale=c["s"], skip=c["skip"],
