@@ -21,6 +21,11 @@ HYMBA_ERR_TIMEOUT = 6
 HYMBA_ERR_DEVICE = 7
 HYMBA_F32 = 0
 HYMBA_BF16 = 1
+HYMBA_ROPE_PAIRS = 0
+HYMBA_ROPE_HALVES = 1
+HYMBA_ROPE_SCALE_NONE = 0
+HYMBA_ROPE_SCALE_LINEAR = 1
+HYMBA_ROPE_SCALE_WAVELENGTH = 2
 
 
 class hymba_layer_config(C.Structure):
@@ -64,6 +69,35 @@ class hymba_block_weights(C.Structure):
 class hymba_prefill_layout(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in ("q", "x_ssm", "gate", "u", "xdbl", "delta", "y_ssm",
                                           "o_attn", "fused", "rope", "sched", "total")]
+
+
+class hymba_rope(C.Structure):
+    _fields_ = [("dim", C.c_int), ("layout", C.c_int), ("scaling", C.c_int), ("attn_factor", C.c_float),
+                ("base", C.c_double), ("factor", C.c_double), ("orig_len", C.c_double),
+                ("low_turns", C.c_double), ("high_turns", C.c_double)]
+
+
+class hymba_head_rows(C.Structure):
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("weight", C.c_void_p),
+                ("in_batch", C.c_int64), ("in_row", C.c_int64), ("in_head", C.c_int64),
+                ("out_batch", C.c_int64), ("out_row", C.c_int64), ("out_head", C.c_int64),
+                ("n_heads", C.c_int)]
+
+
+class hymba_qk_norm_rope_args(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("batch", C.c_int), ("n_rows", C.c_int), ("head_dim", C.c_int),
+                ("q", hymba_head_rows), ("k", hymba_head_rows), ("norm", C.c_int), ("eps", C.c_float),
+                ("rope", hymba_rope), ("pos0", C.c_int64), ("positions", C.c_void_p)]
+
+
+class hymba_linear_attention(C.Structure):
+    _fields_ = ([(n, C.c_int) for n in ("dtype", "batch", "n_rows", "n_heads", "n_qk_heads", "dk", "dv")] +
+                [("scale", C.c_float)] +
+                [f for n, s in (("q", "q"), ("k", "k"), ("v", "v"), ("o", "o"), ("gate", "gate"),
+                                ("log_decay", "decay"), ("in_scale", "scale"))
+                 for f in [(n, C.c_void_p)] + [(f"{s}_{x}", C.c_int64) for x in ("batch", "row", "head")]] +
+                [("skip", C.c_void_p), ("state_in", C.c_void_p), ("state_in_batch", C.c_int64),
+                 ("state_out", C.c_void_p), ("lengths", C.c_void_p)])
 
 
 class hymba_profile_entry(C.Structure):
@@ -115,6 +149,11 @@ _SIGS = {
     "hymba_layer_decode_step": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_void_p, C.c_void_p,
                                           C.POINTER(hymba_kv_cache), C.POINTER(hymba_ssm_cache),
                                           C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hymba_qk_norm_rope": (C.c_int, [C.POINTER(hymba_qk_norm_rope_args), C.c_void_p]),
+    "hymba_linear_attention_workspace": (C.c_int, [C.POINTER(hymba_linear_attention), C.POINTER(C.c_size_t)]),
+    "hymba_linear_attention_prefill": (C.c_int, [C.POINTER(hymba_linear_attention), C.c_void_p, C.c_size_t,
+                                                 C.c_void_p]),
+    "hymba_linear_attention_decode_step": (C.c_int, [C.POINTER(hymba_linear_attention), C.c_void_p]),
     "hymba_stream_status": (C.c_int, [C.c_void_p]),
     "hymba_last_error": (C.c_char_p, []),
     "hymba_status_string": (C.c_char_p, [C.c_int]),
@@ -315,6 +354,27 @@ def hymba_layer_decode_step_static(layer: int, batch: int, pos: int, x_t, y_t,
                                                _stream(stream)), "hymba_layer_decode_step_static")
 
 
+def hymba_qk_norm_rope(args: hymba_qk_norm_rope_args, stream=None) -> None:
+    check(lib().hymba_qk_norm_rope(C.byref(args), _stream(stream)), "hymba_qk_norm_rope")
+
+
+def hymba_linear_attention_workspace(args: hymba_linear_attention) -> int:
+    out = C.c_size_t()
+    check(lib().hymba_linear_attention_workspace(C.byref(args), C.byref(out)), "hymba_linear_attention_workspace")
+    return out.value
+
+
+def hymba_linear_attention_prefill(args: hymba_linear_attention, workspace, workspace_bytes: int,
+                                   stream=None) -> None:
+    check(lib().hymba_linear_attention_prefill(C.byref(args), _ptr(workspace), workspace_bytes, _stream(stream)),
+          "hymba_linear_attention_prefill")
+
+
+def hymba_linear_attention_decode_step(args: hymba_linear_attention, stream=None) -> None:
+    check(lib().hymba_linear_attention_decode_step(C.byref(args), _stream(stream)),
+          "hymba_linear_attention_decode_step")
+
+
 def hymba_stream_status(stream=None) -> None:
     check(lib().hymba_stream_status(_stream(stream)), "hymba_stream_status")
 
@@ -390,3 +450,98 @@ def make_weights(w: dict) -> hymba_layer_weights:
         if not t.is_contiguous():
             raise ValueError(f"weight {k} must be contiguous")
     return hymba_layer_weights(*[_ptr(w[n]) for n, _ in hymba_layer_weights._fields_])
+
+
+def _dtype_of(t) -> int:
+    name = str(t.dtype)
+    if name not in ("torch.bfloat16", "torch.float32"):
+        raise ValueError(f"storage dtype must be bfloat16 or float32, not {name}")
+    return HYMBA_BF16 if name == "torch.bfloat16" else HYMBA_F32
+
+
+def _rows(name: str, t, shape, dtype: str) -> list[int]:
+    """[pointer, batch, row and head stride] of a [batch, rows, heads(, dim)] tensor; checks what
+    the library cannot see: shape, dtype and a contiguous last dimension."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if str(t.dtype) != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.ndim == 4 and shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return [t.data_ptr(), *t.stride()[:3]]
+
+
+def _dense(name: str, t, shape, dtype: str) -> int | None:
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or str(t.dtype) != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected contiguous {tuple(shape)} {dtype}")
+    return t.data_ptr()
+
+
+def make_rope(dim: int, layout: str = "pairs", base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+              orig_len: float = 0.0, low_turns: float = 0.0, high_turns: float = 0.0,
+              attn_factor: float = 1.0) -> hymba_rope:
+    """layout "pairs" or "halves"; scaling "none", "linear" or "wavelength"."""
+    return hymba_rope(dim, {"pairs": HYMBA_ROPE_PAIRS, "halves": HYMBA_ROPE_HALVES}[layout],
+                      {"none": HYMBA_ROPE_SCALE_NONE, "linear": HYMBA_ROPE_SCALE_LINEAR,
+                       "wavelength": HYMBA_ROPE_SCALE_WAVELENGTH}[scaling],
+                      attn_factor, base, factor, orig_len, low_turns, high_turns)
+
+
+def make_qk_norm_rope(q, k, q_out=None, k_out=None, norm: bool = True, eps: float = 1e-6, q_weight=None,
+                      k_weight=None, rope: hymba_rope | None = None, pos0: int = 0,
+                      positions=None) -> hymba_qk_norm_rope_args:
+    """q [batch, rows, heads, dim], k [batch, rows, kv_heads, dim] or None: device tensors of any
+    strides with a contiguous head; q_out, k_out likewise (None: in place).  The description holds
+    addresses only: the tensors must outlive its use."""
+    some = q if q is not None else k
+    B, R, _, d = some.shape
+    a = hymba_qk_norm_rope_args(dtype=_dtype_of(some), batch=B, n_rows=R, head_dim=d, norm=int(norm), eps=eps,
+                                pos0=pos0)
+    for side, x, out, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+        if x is None:
+            continue
+        shape = (B, R, x.shape[2], d)
+        i = _rows(side, x, shape, str(some.dtype))
+        o = _rows(side + "_out", x if out is None else out, shape, str(some.dtype))
+        setattr(a, side, hymba_head_rows(i[0], o[0], _dense(side + "_weight", w, (d,), "torch.float32"), *i[1:], *o[1:],
+                                         x.shape[2]))
+    if rope is not None:
+        a.rope = rope
+    a.positions = _dense("positions", positions, (B, R), "torch.int64")
+    return a
+
+
+def make_linear_attention(q, k, v, o, log_decay=None, in_scale=None, skip=None, gate=None, state_in=None,
+                          state_out=None, lengths=None, scale: float = 1.0) -> hymba_linear_attention:
+    """q, k [batch, rows, qk_heads, dk], v, o, gate [batch, rows, heads, dv]: device tensors of any
+    strides with a contiguous head; log_decay, in_scale [batch, rows, heads] fp32 of any strides
+    (expand() repeats a value); skip [heads, dv]; state_in [batch, heads, dv, dk] dense per sequence
+    (expand() over the batch repeats one); state_out likewise, dense; lengths [batch] int32.  The
+    description holds addresses only: the tensors must outlive its use."""
+    B, L, K, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    dt = str(q.dtype)
+    a = hymba_linear_attention(dtype=_dtype_of(q), batch=B, n_rows=L, n_heads=H, n_qk_heads=K, dk=dk, dv=dv,
+                               scale=scale)
+    grids = (("q", "q", q, (B, L, K, dk), dt), ("k", "k", k, (B, L, K, dk), dt), ("v", "v", v, (B, L, H, dv), dt),
+             ("o", "o", o, (B, L, H, dv), dt), ("gate", "gate", gate, (B, L, H, dv), dt),
+             ("log_decay", "decay", log_decay, (B, L, H), "torch.float32"),
+             ("in_scale", "scale", in_scale, (B, L, H), "torch.float32"))
+    for name, stride, t, shape, want in grids:
+        if t is not None:
+            p, sb, sr, sh = _rows(name, t, shape, want)
+            setattr(a, name, p)
+            setattr(a, stride + "_batch", sb)
+            setattr(a, stride + "_row", sr)
+            setattr(a, stride + "_head", sh)
+    a.skip = _dense("skip", skip, (H, dv), "torch.float32")
+    if state_in is not None:
+        if tuple(state_in.shape) != (B, H, dv, dk):
+            raise ValueError(f"state_in: shape {tuple(state_in.shape)}, expected {(B, H, dv, dk)}")
+        a.state_in = _dense("state_in[0]", state_in[0], (H, dv, dk), "torch.float32")
+        a.state_in_batch = state_in.stride(0)
+    a.state_out = _dense("state_out", state_out, (B, H, dv, dk), "torch.float32")
+    a.lengths = _dense("lengths", lengths, (B,), "torch.int32")
+    return a

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "profile.h"
 
 namespace hymba {
 
@@ -22,6 +23,7 @@ static thread_local char g_msg[512] = "";
 
 static std::atomic<unsigned long long> g_launches{0};
 void note_launch(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
+unsigned long long launches_noted() { return g_launches.load(); }
 
 constexpr long long kDefaultWaitLimit = 1000000000LL;  // ~0.5 s at 2 GHz
 constexpr long long kMinWaitLimit = 100000LL;
@@ -78,60 +80,11 @@ void set_error(const char *fmt, ...) {
 
 using namespace hymba;
 
-// ---------------------------------------------------------------------------
-// Optional per-step timing with CUDA events (hymba_profile_enable).
-// ---------------------------------------------------------------------------
-namespace {
-struct ProfRecord {
-  const char *name;
-  cudaEvent_t start, stop;
-  unsigned long long kernels;
-};
-struct Profiler {
-  std::mutex mu;
-  bool on = false;
-  std::vector<cudaEvent_t> pool;
-  size_t next = 0;
-  std::vector<ProfRecord> recs;
-};
-Profiler &prof() {
+Profiler &hymba::prof() {
   static Profiler p;
   return p;
 }
 constexpr size_t kProfEvents = 8192;
-
-class ProfScope {
- public:
-  ProfScope(cudaStream_t s, const char *name) : s_(s) {
-    Profiler &p = prof();
-    if (!p.on) return;
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) return;
-    std::lock_guard<std::mutex> g(p.mu);
-    if (p.next + 2 > p.pool.size()) return;  // pool exhausted: stop recording until collected
-    rec_.name = name;
-    launches0_ = g_launches.load();
-    rec_.start = p.pool[p.next++];
-    rec_.stop = p.pool[p.next++];
-    cudaEventRecord(rec_.start, s_);
-    active_ = true;
-  }
-  ~ProfScope() {
-    if (!active_) return;
-    cudaEventRecord(rec_.stop, s_);
-    rec_.kernels = g_launches.load() - launches0_;
-    Profiler &p = prof();
-    std::lock_guard<std::mutex> g(p.mu);
-    p.recs.push_back(rec_);
-  }
-
- private:
-  cudaStream_t s_;
-  ProfRecord rec_{};
-  unsigned long long launches0_ = 0;
-  bool active_ = false;
-};
-}  // namespace
 
 // Side stream of the concurrent prefill (branch_chunks >= 2) and its events: one fork
 // event, then per chunk one after its dt_proj and one after its scan.

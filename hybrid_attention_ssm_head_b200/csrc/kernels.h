@@ -297,6 +297,16 @@ hymba_status decode_conv_xproj(const DecodeSsmArgs &a, hymba_dtype dt, cudaStrea
 // delta = softplus(delta_r W_dt^T + b_dt), one recurrence step, y = (C.h + D u) * gate.
 hymba_status decode_scan(const DecodeSsmArgs &a, hymba_dtype dt, cudaStream_t s);
 
+// ---- operators on rows of heads (arguments validated by the ABI layer) ----------------
+hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s);
+// One row per sequence (a.n_rows == 1).
+hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s);
+// Whole sequences; workspace of linear_attention_workspace_bytes(a) bytes.
+hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s);
+size_t linear_attention_workspace_bytes(const hymba_linear_attention &a);
+// A rotation's own numbers, for heads of `width` elements.
+hymba_status check_rope(const hymba_rope &r, int width);
+
 hymba_status mask_bitmap(int L, int n_meta, int window, int is_global, int path, uint32_t *bits,
                          uint8_t *tile_class, cudaStream_t s);
 // The decode kernels' slot predicate for the query at `pos`, one bit per slot.

@@ -1,0 +1,299 @@
+// Linear attention with a decay for each head, on the CUDA cores (hymba_linear_attention_*):
+//   S_t = exp(g_t) S_{t-1} + s_t v_t k_t^T,   o_t = (scale S_t q_t + skip v_t) gate_t
+// The state S [dv, dk] is fp32 throughout.
+#include "common.cuh"
+#include "linattn.cuh"
+
+namespace hymba {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// one token per sequence
+// ---------------------------------------------------------------------------
+constexpr int kStepWarps = 8;
+constexpr int kStepAhead = 8;  // 16-byte state loads in flight per lane
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
+  if constexpr (sizeof(T) == 2) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  } else {
+    return *reinterpret_cast<const float4 *>(p);
+  }
+}
+
+// Bound by the state's bytes, read and written once.  A CTA takes `rows` of the dv state
+// rows of one (sequence, head); `lanes` lanes (a power of two) hold one row, four columns
+// each, so a warp's loads and stores are whole contiguous rows.
+template <typename T>
+__global__ void __launch_bounds__(32 * kStepWarps)
+    linear_step_kernel(const __grid_constant__ hymba_linear_attention a, int lanes, int rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int hk = h / (a.n_heads / a.n_qk_heads);
+  const int lane = lane_id(), li = lane & (lanes - 1), c0 = 4 * li;
+  const bool live = c0 < a.dk;
+  const int per = 32 / lanes;  // state rows per warp and load
+  const int p_end = min(a.dv, (int)(blockIdx.x + 1) * rows);
+  const long long dense = (long long)a.dv * a.dk;
+  const float *sin = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
+  float *sout = a.state_out + ((long long)b * a.n_heads + h) * dense;
+  const bool idle = a.lengths && a.lengths[b] <= 0;
+  if (idle && sin == sout) return;
+  const float decay = a.log_decay ? linear_decay(a.log_decay[b * a.decay_batch + h * a.decay_head]) : 1.f;
+  const float s = a.in_scale ? a.in_scale[b * a.scale_batch + h * a.scale_head] : 1.f;
+  const T *vp = reinterpret_cast<const T *>(a.v) + b * a.v_batch + h * a.v_head;
+  T *op = reinterpret_cast<T *>(a.o) + b * a.o_batch + h * a.o_head;
+  const T *zp = reinterpret_cast<const T *>(a.gate) + (a.gate ? b * a.gate_batch + h * a.gate_head : 0);
+  float4 k = make_float4(0.f, 0.f, 0.f, 0.f), q = k;
+  if (live) {
+    k = load4(reinterpret_cast<const T *>(a.k) + b * a.k_batch + hk * a.k_head + c0);
+    q = load4(reinterpret_cast<const T *>(a.q) + b * a.q_batch + hk * a.q_head + c0);
+  }
+  const int stride = kStepWarps * per;
+  for (int p0 = blockIdx.x * rows + warp_id() * per + lane / lanes; p0 - lane / lanes < p_end;
+       p0 += kStepAhead * stride) {
+    float4 st[kStepAhead];
+    float v[kStepAhead];
+#pragma unroll
+    for (int u = 0; u < kStepAhead; ++u) {
+      const int p = p0 + u * stride;
+      st[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = 0.f;
+      if (p < p_end) {
+        if (live && sin) st[u] = *reinterpret_cast<const float4 *>(sin + (long long)p * a.dk + c0);
+        v[u] = Store<T>::to_f(vp[p]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kStepAhead; ++u) {
+      const int p = p0 + u * stride;
+      const float x = s * v[u];
+      if (!idle) {
+        st[u].x = fmaf(decay, st[u].x, x * k.x);
+        st[u].y = fmaf(decay, st[u].y, x * k.y);
+        st[u].z = fmaf(decay, st[u].z, x * k.z);
+        st[u].w = fmaf(decay, st[u].w, x * k.w);
+      }
+      float dot = fmaf(st[u].x, q.x, st[u].y * q.y) + fmaf(st[u].z, q.z, st[u].w * q.w);
+      for (int m = lanes >> 1; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+      if (p < p_end) {
+        if (live) *reinterpret_cast<float4 *>(sout + (long long)p * a.dk + c0) = st[u];
+        if (li == 0 && !idle) {
+          float y = a.scale * dot;
+          if (a.skip) y = fmaf(a.skip[(long long)h * a.dv + p], v[u], y);
+          if (a.gate) y *= Store<T>::to_f(zp[p]);
+          op[p] = Store<T>::from_f(y);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// row by row
+// ---------------------------------------------------------------------------
+constexpr int kScanRows = 16;   // rows staged at a time
+constexpr int kFix = 8;         // rows between corrections of the decays
+constexpr int kScanState = 64;  // state rows per CTA (two per thread group)
+
+// NC columns of two adjacent state rows per thread, CL threads per row pair: the state stays
+// in registers as fp32 pairs.  q, k, v, the gate and the decays of kScanRows rows are staged
+// in shared memory as fp32.
+//
+// Decays near one: a fp32 decay is off by up to 2^-25, the same way at every row of a head
+// with one fixed decay, so their product drifts from exp(sum g) by 2^-25 times the rows.
+// The staged decays are therefore corrected every kFix rows: exp(sum g) over the product used
+// so far is carried in fp64, and the next group's first decay takes it up.
+template <typename T, int NC, int CL>
+__global__ void __launch_bounds__(kScanState / 2 * CL)
+    linear_scan_kernel(const __grid_constant__ hymba_linear_attention a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int THR = kScanState / 2 * CL, DK = NC * CL;
+  static_assert(THR >= 32, "one warp stages the decays");
+  __shared__ __align__(16) float s_q[kScanRows][DK], s_k[kScanRows][DK];
+  __shared__ __align__(8) float s_v[kScanRows][kScanState], s_z[kScanRows][kScanState];
+  __shared__ float2 s_dx[kScanRows];  // (decay, input scale)
+  const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int hk = h / (a.n_heads / a.n_qk_heads);
+  const int pb = blockIdx.x * kScanState;              // the CTA's first state row
+  const int pn = min(kScanState, a.dv - pb);           // and how many (even)
+  const int pr = 2 * (tid / CL), c0 = (tid % CL) * NC; // this thread's row pair and columns
+  const bool rows_live = pr < pn;
+  const int L = linear_length(a, b);
+  const long long dense = (long long)a.dv * a.dk;
+  const T *qp = reinterpret_cast<const T *>(a.q) + b * a.q_batch + hk * a.q_head;
+  const T *kp = reinterpret_cast<const T *>(a.k) + b * a.k_batch + hk * a.k_head;
+  const T *vp = reinterpret_cast<const T *>(a.v) + b * a.v_batch + h * a.v_head + pb;
+  const T *zp = reinterpret_cast<const T *>(a.gate) + (a.gate ? b * a.gate_batch + h * a.gate_head + pb : 0);
+  T *op = reinterpret_cast<T *>(a.o) + b * a.o_batch + h * a.o_head + pb;
+  const float *gp = a.log_decay ? a.log_decay + b * a.decay_batch + h * a.decay_head : nullptr;
+  const float *sp = a.in_scale ? a.in_scale + b * a.scale_batch + h * a.scale_head : nullptr;
+
+  float2 S[2][NC / 2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < NC; c += 4) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.state_in && rows_live && c0 + c < a.dk)
+        x = *reinterpret_cast<const float4 *>(a.state_in + b * a.state_in_batch + h * dense +
+                                              (long long)(pb + pr + r) * a.dk + c0 + c);
+      S[r][c / 2] = make_float2(x.x, x.y);
+      S[r][c / 2 + 1] = make_float2(x.z, x.w);
+    }
+  float2 skip = make_float2(0.f, 0.f);
+  if (a.skip && rows_live) skip = *reinterpret_cast<const float2 *>(a.skip + (long long)h * a.dv + pb + pr);
+
+  double carry = 1.0;  // exp(sum g) over the product of the decays used so far
+  for (int t0 = 0; t0 < L; t0 += kScanRows) {
+    const int nt = min(kScanRows, L - t0);
+    __syncthreads();
+    for (int i = tid; i < nt * (DK / 4); i += THR) {
+      const int t = i / (DK / 4), c = 4 * (i % (DK / 4));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (c < a.dk) {
+        x = load4(qp + (t0 + t) * a.q_row + c);
+        y = load4(kp + (t0 + t) * a.k_row + c);
+      }
+      *reinterpret_cast<float4 *>(&s_q[t][c]) = x;
+      *reinterpret_cast<float4 *>(&s_k[t][c]) = y;
+    }
+    for (int i = tid; i < nt * (kScanState / 4); i += THR) {
+      const int t = i / (kScanState / 4), c = 4 * (i % (kScanState / 4));
+      if (c < pn) {
+        *reinterpret_cast<float4 *>(&s_v[t][c]) = load4(vp + (t0 + t) * a.v_row + c);
+        if (a.gate) *reinterpret_cast<float4 *>(&s_z[t][c]) = load4(zp + (t0 + t) * a.gate_row + c);
+      }
+    }
+    if (tid < 32) {
+      const int t = tid;
+      double want = 1.0;
+      if (t < nt && gp) want = linear_decay64(gp[(t0 + t) * a.decay_row]);
+      float used = (float)want;
+      // what the rounding of the other rows of this group of kFix leaves over; then each
+      // group's first decay in turn takes up what was left over before it
+      double left = t % kFix && used > 0.f ? want / (double)used : 1.0;
+#pragma unroll
+      for (int m = kFix >> 1; m > 0; m >>= 1) left *= __shfl_xor_sync(0xffffffffu, left, m);
+#pragma unroll
+      for (int f = 0; f < kScanRows; f += kFix) {
+        double next = carry;
+        if (t == f) {
+          const double exact = want * carry;
+          used = (float)exact;
+          next = (used > 0.f ? exact / (double)used : 1.0) * left;
+        }
+        carry = __shfl_sync(0xffffffffu, next, f);
+      }
+      if (t < nt) s_dx[t] = make_float2(used, sp ? sp[(t0 + t) * a.scale_row] : 1.f);
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+      const float2 dx = s_dx[t];
+      const float2 v = *reinterpret_cast<const float2 *>(&s_v[t][pr]);
+      const float2 d2 = make_float2(dx.x, dx.x);
+      const float2 x0 = make_float2(dx.y * v.x, dx.y * v.x), x1 = make_float2(dx.y * v.y, dx.y * v.y);
+      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+      for (int c = 0; c < NC; c += 4) {
+        const float4 k = *reinterpret_cast<const float4 *>(&s_k[t][c0 + c]);
+        const float4 q = *reinterpret_cast<const float4 *>(&s_q[t][c0 + c]);
+        const float2 ka = make_float2(k.x, k.y), kb = make_float2(k.z, k.w);
+        const float2 qa = make_float2(q.x, q.y), qb = make_float2(q.z, q.w);
+        S[0][c / 2] = ffma2(d2, S[0][c / 2], fmul2(x0, ka));
+        S[0][c / 2 + 1] = ffma2(d2, S[0][c / 2 + 1], fmul2(x0, kb));
+        S[1][c / 2] = ffma2(d2, S[1][c / 2], fmul2(x1, ka));
+        S[1][c / 2 + 1] = ffma2(d2, S[1][c / 2 + 1], fmul2(x1, kb));
+        acc0 = ffma2(S[0][c / 2], qa, acc0);
+        acc1 = ffma2(S[1][c / 2], qa, acc1);
+        acc0 = ffma2(S[0][c / 2 + 1], qb, acc0);
+        acc1 = ffma2(S[1][c / 2 + 1], qb, acc1);
+      }
+      float y0 = acc0.x + acc0.y, y1 = acc1.x + acc1.y;
+#pragma unroll
+      for (int m = CL >> 1; m > 0; m >>= 1) {
+        y0 += __shfl_xor_sync(0xffffffffu, y0, m);
+        y1 += __shfl_xor_sync(0xffffffffu, y1, m);
+      }
+      if (tid % CL == 0 && rows_live) {
+        y0 = fmaf(skip.x, v.x, a.scale * y0);
+        y1 = fmaf(skip.y, v.y, a.scale * y1);
+        if (a.gate) {
+          const float2 z = *reinterpret_cast<const float2 *>(&s_z[t][pr]);
+          y0 *= z.x;
+          y1 *= z.y;
+        }
+        T *o = op + (t0 + t) * a.o_row + pr;
+        if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t *>(o) = pack_bf16x2(y0, y1);
+        else *reinterpret_cast<float2 *>(o) = make_float2(y0, y1);
+      }
+    }
+  }
+  if (a.state_out && rows_live) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < NC; c += 4)
+        if (c0 + c < a.dk)
+          *reinterpret_cast<float4 *>(a.state_out + ((long long)b * a.n_heads + h) * dense +
+                                      (long long)(pb + pr + r) * a.dk + c0 + c) =
+              make_float4(S[r][c / 2].x, S[r][c / 2].y, S[r][c / 2 + 1].x, S[r][c / 2 + 1].y);
+  }
+}
+
+hymba_status launched(const char *what) {
+  note_launch(1);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("%s launch failed: %s", what, cudaGetErrorString(e));
+    return HYMBA_ERR_CUDA;
+  }
+  return HYMBA_OK;
+}
+
+template <typename T>
+void scan_launch(const hymba_linear_attention &a, cudaStream_t s) {
+  const dim3 grid((a.dv + kScanState - 1) / kScanState, a.n_heads, a.batch);
+  constexpr int one = kScanState / 2;
+  if (a.dk <= 16) launch_kernel(linear_scan_kernel<T, 16, 1>, grid, dim3(one), 0, s, a);
+  else if (a.dk <= 32) launch_kernel(linear_scan_kernel<T, 32, 1>, grid, dim3(one), 0, s, a);
+  else if (a.dk <= 64) launch_kernel(linear_scan_kernel<T, 32, 2>, grid, dim3(2 * one), 0, s, a);
+  else launch_kernel(linear_scan_kernel<T, 32, 4>, grid, dim3(4 * one), 0, s, a);
+}
+
+}  // namespace
+
+hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s) {
+  int lanes = 1;
+  while (lanes * 4 < a.dk) lanes *= 2;
+  // One CTA for all state rows of a (sequence, head) keeps eight loads in flight per lane;
+  // with fewer (sequence, head) pairs than two CTAs for each SM the rows are split, down to
+  // one load per lane.
+  const int once = kStepWarps * (32 / lanes);
+  const int most = (a.dv + once - 1) / once;
+  const long long pairs = (long long)a.batch * a.n_heads;
+  const long long want = (2 * 148 + pairs - 1) / pairs;
+  const int parts = int(want < most ? want : most);
+  const int rows = (most + parts - 1) / parts * once;
+  const dim3 grid((a.dv + rows - 1) / rows, a.n_heads, a.batch);
+  if (a.dtype == HYMBA_BF16)
+    launch_kernel(linear_step_kernel<__nv_bfloat16>, grid, dim3(32 * kStepWarps), 0, s, a, lanes, rows);
+  else
+    launch_kernel(linear_step_kernel<float>, grid, dim3(32 * kStepWarps), 0, s, a, lanes, rows);
+  return launched("linear attention step");
+}
+
+size_t linear_attention_workspace_bytes(const hymba_linear_attention &) { return 0; }
+
+hymba_status linear_attention(const hymba_linear_attention &a, void *, cudaStream_t s) {
+  if (a.dtype == HYMBA_BF16) scan_launch<__nv_bfloat16>(a, s);
+  else scan_launch<float>(a, s);
+  return launched("linear attention");
+}
+
+}  // namespace hymba

@@ -365,6 +365,143 @@ HYMBA_API hymba_status hymba_block_decode_step(hymba_layer *layer, const hymba_b
                                                hymba_kv_cache *kv_cache, hymba_ssm_cache *ssm_cache,
                                                void *workspace, size_t workspace_bytes, hymba_stream_t stream);
 
+/* ---- operators: head norm and rotation ---------------------------------------- */
+
+/* The operators below work on rows of heads: a [batch, n_rows, n_heads, dim] grid given by a
+ * pointer and the element strides between sequences, rows and heads (a head's dim elements
+ * are contiguous).  Unlike the layer calls' densely packed tensors, any strides are taken
+ * that keep every head 16-byte aligned, so that heads can be read and written where another
+ * step left them: side by side in a fused projection, or in the slots of a K/V store.  The
+ * written elements of one grid must not overlap each other (checked), nor any input other
+ * than as stated (the caller's duty).  A stride over an extent of one is not looked at. */
+
+/* Position rotation of a head's first `dim` elements: pair i of dim / 2 is turned by the
+ * angle p * f_i at position p (§2.5 changes "the RoPE base" for longer contexts), and scaled:
+ *     (a, b) -> attn_factor (a cos - b sin, a sin + b cos)
+ *   layout   HYMBA_ROPE_PAIRS: pair i is elements (2i, 2i+1);
+ *            HYMBA_ROPE_HALVES: elements (i, i + dim/2)
+ *   f_i      base^(-2i/dim), then by `scaling`:
+ *     HYMBA_ROPE_SCALE_NONE        as it is
+ *     HYMBA_ROPE_SCALE_LINEAR      f_i / factor: positions of a context `factor` times longer
+ *                                  are squeezed into the trained range
+ *     HYMBA_ROPE_SCALE_WAVELENGTH  by the turns r = orig_len f_i / 2 pi a pair makes over the
+ *                                  trained length: f_i for r >= high_turns, f_i / factor for
+ *                                  r <= low_turns, and linear in r between
+ * dim even, 0 for no rotation, at most the head's; base > 1; factor, attn_factor > 0.  Angles
+ * are computed in fp64, so far positions keep their accuracy. */
+enum { HYMBA_ROPE_PAIRS = 0, HYMBA_ROPE_HALVES = 1 };
+enum { HYMBA_ROPE_SCALE_NONE = 0, HYMBA_ROPE_SCALE_LINEAR = 1, HYMBA_ROPE_SCALE_WAVELENGTH = 2 };
+typedef struct {
+  int dim;
+  int layout;
+  int scaling;
+  float attn_factor;
+  double base;
+  double factor;
+  double orig_len;
+  double low_turns, high_turns;
+} hymba_rope;
+
+/* Heads read from `in` and written to `out` (which may be `in` with the same strides: in
+ * place; otherwise the two must not overlap).  weight [head_dim] fp32 or NULL. */
+typedef struct {
+  const void *in;
+  void *out;
+  const float *weight;
+  int64_t in_batch, in_row, in_head;
+  int64_t out_batch, out_row, out_head;
+  int n_heads;   /* 0: none (pointers and strides not looked at) */
+} hymba_head_rows;
+
+/* Norm and rotation of the query and key heads in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight     over each head's head_dim elements (norm = 1)
+ *     y = x                                      (norm = 0; weights must be NULL)
+ * then the rotation of y to its row's position.  Computed in fp32 with one rounding to the
+ * storage type.  Row r of sequence b is at position pos0 + r, or at positions[b, r]
+ * (device, dense [batch, n_rows]; added to pos0).  head_dim a multiple of 8, at most 256. */
+typedef struct {
+  hymba_dtype dtype;
+  int batch, n_rows, head_dim;
+  hymba_head_rows q, k;
+  int norm;
+  float eps;
+  hymba_rope rope;
+  int64_t pos0;
+  const int64_t *positions; /* optional */
+} hymba_qk_norm_rope_args;
+
+/* Asynchronous on `stream`; no workspace.  INVALID_ARG / UNSUPPORTED before any launch. */
+HYMBA_API hymba_status hymba_qk_norm_rope(const hymba_qk_norm_rope_args *args, hymba_stream_t stream);
+
+/* ---- operators: linear attention ------------------------------------------------ */
+
+/* Linear attention with a decay for each head: the recurrence of Eq. 2 with one decay for a
+ * whole head instead of one for each (channel, state) pair.  The paper's comparison of SSM
+ * heads names this form (the OpenReview reply on Mamba2 heads).  For each sequence and head h,
+ * reading query/key head h / (n_heads / n_qk_heads):
+ *     S_t = exp(g_t) S_{t-1} + s_t v_t k_t^T           S: [dv, dk], fp32
+ *     o_t = (scale S_t q_t + skip v_t) gate_t
+ *   q, k       [batch, n_rows, n_qk_heads, dk] dtype
+ *   v, o       [batch, n_rows, n_heads, dv] dtype
+ *   gate       as v, or NULL (1)
+ *   log_decay  g [batch, n_rows, n_heads] fp32, any strides >= 0 (0 repeats a value: one decay
+ *              for each head), or NULL (no decay).  g <= 0; below -110, -infinity included,
+ *              the state is forgotten (exp(g) is 0 in fp32), as at the start of a document.
+ *   in_scale   s, likewise, or NULL (1)
+ *   skip       [n_heads, dv] fp32 or NULL (0)
+ *   state_in   S_0, each sequence's [n_heads, dv, dk] dense, state_in_batch floats apart (0: one
+ *              state for every sequence), or NULL (zero)
+ *   state_out  the state after the last row, [batch, n_heads, dv, dk] dense, or NULL.  May be
+ *              state_in (in place, state_in_batch = n_heads dv dk); otherwise no overlap.
+ *   lengths    [batch] int32 (device) or NULL: rows from lengths[b] on (clamped to 0..n_rows)
+ *              do not change the state of sequence b, and their o is left as it was, whatever
+ *              their inputs hold, infinities and NaN included.
+ * dk a multiple of 8 up to 128, dv a multiple of 8 up to 256.  q, k, v, o, gate: strides > 0
+ * where the extent is above one.  o must not overlap any input.
+ * A non-finite value in a row reaches that row's output and the rows after it; in
+ * hymba_linear_attention_prefill with bf16 storage a non-finite v_t may also reach the
+ * outputs of the up to 127 rows before row t, which are computed together with it. */
+typedef struct {
+  hymba_dtype dtype;
+  int batch, n_rows, n_heads, n_qk_heads, dk, dv;
+  float scale;
+  const void *q;
+  int64_t q_batch, q_row, q_head;
+  const void *k;
+  int64_t k_batch, k_row, k_head;
+  const void *v;
+  int64_t v_batch, v_row, v_head;
+  void *o;
+  int64_t o_batch, o_row, o_head;
+  const void *gate;
+  int64_t gate_batch, gate_row, gate_head;
+  const float *log_decay;
+  int64_t decay_batch, decay_row, decay_head;
+  const float *in_scale;
+  int64_t scale_batch, scale_row, scale_head;
+  const float *skip;
+  const float *state_in;
+  int64_t state_in_batch;
+  float *state_out;
+  const int32_t *lengths;
+} hymba_linear_attention;
+
+/* Bytes of device workspace hymba_linear_attention_prefill needs for these sizes (0 for some:
+ * the workspace may then be NULL).  Reads the sizes, the dtype and which pointers are NULL. */
+HYMBA_API hymba_status hymba_linear_attention_workspace(const hymba_linear_attention *args, size_t *bytes);
+
+/* Whole sequences (a prompt, or some rows continuing a stored state).  Asynchronous on
+ * `stream`; workspace 256-byte aligned, its contents need not be kept between calls, and
+ * calls that may overlap on the GPU need one each (two captured graphs included). */
+HYMBA_API hymba_status hymba_linear_attention_prefill(const hymba_linear_attention *args, void *workspace,
+                                                      size_t workspace_bytes, hymba_stream_t stream);
+
+/* One token per sequence (n_rows = 1, state_out required): one step of the recurrence on the
+ * stored state, without a workspace.  A sequence whose length is 0 is idle: its state is kept
+ * (copied when state_out is not state_in) and its o left as it was. */
+HYMBA_API hymba_status hymba_linear_attention_decode_step(const hymba_linear_attention *args,
+                                                          hymba_stream_t stream);
+
 /* ---- status and diagnostics -------------------------------------------- */
 
 /* Synchronises `stream`, then reports a pending CUDA error or a device-side
