@@ -1338,7 +1338,7 @@ hymba_status hymba_stream_status(hymba_stream_t stream) {
   if (e != cudaSuccess) FAIL(HYMBA_ERR_CUDA, "%s", cudaGetErrorString(e));
   e = cudaGetLastError();
   if (e != cudaSuccess) FAIL(HYMBA_ERR_CUDA, "%s", cudaGetErrorString(e));
-  const unsigned err = take_error_gemm() | take_error_attn();
+  const unsigned err = take_error_gemm() | take_error_attn() | take_error_linear();
   if (err & kErrTimeoutHost) FAIL(HYMBA_ERR_TIMEOUT, "a device-side wait timed out");
   return HYMBA_OK;
 }

@@ -303,6 +303,8 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s);
 hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s);
 // Whole sequences; workspace of linear_attention_workspace_bytes(a) bytes.
 hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s);
+// ... of bf16 storage on the tensor cores.
+hymba_status linear_attention_tc(const hymba_linear_attention &a, cudaStream_t s);
 size_t linear_attention_workspace_bytes(const hymba_linear_attention &a);
 // A rotation's own numbers, for heads of `width` elements.
 hymba_status check_rope(const hymba_rope &r, int width);
@@ -329,6 +331,7 @@ constexpr unsigned kErrTimeoutHost = 1u;
 // Device error words of every translation unit: read and clear.
 unsigned take_error_gemm();
 unsigned take_error_attn();
+unsigned take_error_linear();
 
 // Counts kernel launches of this library (for the optional profiler).
 void note_launch(int n = 1);

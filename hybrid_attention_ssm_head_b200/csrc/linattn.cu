@@ -291,8 +291,8 @@ hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t
 size_t linear_attention_workspace_bytes(const hymba_linear_attention &) { return 0; }
 
 hymba_status linear_attention(const hymba_linear_attention &a, void *, cudaStream_t s) {
-  if (a.dtype == HYMBA_BF16) scan_launch<__nv_bfloat16>(a, s);
-  else scan_launch<float>(a, s);
+  if (a.dtype == HYMBA_BF16) return linear_attention_tc(a, s);
+  scan_launch<float>(a, s);
   return launched("linear attention");
 }
 

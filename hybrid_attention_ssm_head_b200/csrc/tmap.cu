@@ -31,8 +31,8 @@ bool make_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, in
     set_error("cuTensorMapEncodeTiled unavailable (no CUDA driver?)");
     return false;
   }
-  cuuint64_t d[3], st[2];
-  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     bx[i] = box[i];

@@ -8,7 +8,7 @@
 
 namespace hymba {
 
-// 128-byte swizzled tiled map of a row-major tensor with up to 3 dims.
+// 128-byte swizzled tiled map of a row-major tensor with up to 4 dims.
 // dims[0] is the contiguous dimension (elements); strides_bytes[i] is the byte
 // stride of dims[i+1].  box[i] elements per copy.  Out-of-range elements read 0.
 bool make_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank,

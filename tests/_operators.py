@@ -85,12 +85,12 @@ def linear_bounds(dtype, L, dk, want, size, state, state_size, chunked):
     once each, as does the decay itself, so behind L rows a state is within (4 L + 8) half steps of
     its size; the dot product over dk columns adds dk + 8.  bf16 storage rounds o once more
     (half a bf16 step of o).  The chunked form, where one is used, rounds each score to bf16 once
-    (half a bf16 step of the size) and multiplies with states and keys split in two bf16 parts,
-    which leaves 2^-16 of each term."""
+    (half a bf16 step of the size) and multiplies with states split in two bf16 parts, which leaves
+    2^-16 of each term, and with keys split in three, which leaves 2^-24."""
     rho = (4 * L + dk + 16) * F32_STEP
     if chunked:
         return (BF16_STEP * want.abs() + (BF16_STEP + 2 * 2.0 ** -16 + rho) * size + 1e-30,
-                (2.0 ** -16 + rho) * state_size + 1e-30)
+                rho * state_size + 1e-30)
     return half_step(dtype) * want.abs() + rho * size + 1e-30, rho * state_size + 1e-30
 
 
