@@ -22,10 +22,10 @@ HYMBA_DEVICE_ERROR_WORD(g_err_lin);
 namespace {
 
 constexpr int C = 128;         // rows per chunk
-constexpr int kThreads = 384;  // TMA, MMA and decay warps (+ one idle), scores, state
-constexpr int kRegCtrl = 72, kRegWork = 216;  // 128 * 72 + 256 * 216 = 384 * 168
+constexpr int kThreads = 512;  // TMA, MMA and decay warps (+ one idle), scores, state, output
+constexpr int kRegCtrl = 56, kRegScores = 144, kRegState = 184, kRegOut = 128;
+static_assert(kRegCtrl + kRegScores + kRegState + kRegOut == 4 * 128, "the warpgroups share 512 x 128 registers");
 constexpr int kAtom = C * 128;  // bytes of 128 rows x 64 bf16 columns, 128-byte swizzle
-constexpr float kLog2eF = 1.4426950408889634f;
 
 struct Decays {  // of one chunk's rows, log2 units
   float hi[C], lo[C];  // G = hi + lo, hi a multiple of 1/8: differences of hi are exact
@@ -35,35 +35,60 @@ struct Decays {  // of one chunk's rows, log2 units
   float e[C];          // exp(G)
 };
 
-// NK, NV: 64-column atoms of dk and of the CTA's dv block.  Two stages of (Q, K, V) tiles
-// and a gate tile fit shared memory for dk <= 64; wider keys take one stage, and read the
-// gate from global memory.
+// NK, NV: 64-column atoms of dk and of the CTA's dv block.  For dk <= 64 two stages of
+// (Q, K, V) tiles fit shared memory, and a tile that the gate is loaded into and the output
+// is stored from.  Wider keys take one stage, stage the output over V and read the gate from
+// global memory.
 template <int NK, int NV>
 struct Layout {
   static constexpr int STAGES = NK == 1 ? 2 : 1;
-  static constexpr bool GATE = NK == 1;
+  static constexpr bool TILE = NK == 1;
   static constexpr int Q = 0, K = NK * kAtom, V = 2 * NK * kAtom, STAGE = (2 * NK + NV) * kAtom;
   static constexpr int MID = STAGES * STAGE;            // middle parts of the weighted keys
   static constexpr int SB = MID + NK * kAtom;           // state operand: hi, then lo
   static constexpr int SB_PART = NK * NV * (kAtom / 2); // 64 NV rows of 128 bytes per dk atom
-  static constexpr int Z = SB + 2 * SB_PART;            // gate tile
+  static constexpr int Z = SB + 2 * SB_PART;            // gate and output tile
   // the state product reads 128 state rows whatever dv is: for NV = 1 up to one atom behind V
-  static constexpr int DEC = Z + (GATE ? NV * kAtom : 0);
+  static constexpr int DEC = Z + (TILE ? NV * kAtom : 0);
   static constexpr int SKIP = DEC + 2 * (int)sizeof(Decays);
   static constexpr int BAR = SKIP + NV * 64 * 4;
   static constexpr int TOTAL = BAR + 32 * 8 + 1024;  // + alignment of the base
 };
 
+// Two fp32 values cut to their high 16 bits, as a bf16 pair: what is cut off is exact in fp32,
+// so three such parts hold all 24 bits of a value.
+__device__ __forceinline__ uint32_t high_pair(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+
+// A bounded wait as in common.cuh, in few instructions: the roles' loops have to stay in the
+// instruction cache together (see the kernel).  A CTA that starts after another has given up
+// does nothing.
+__device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, unsigned limit) {
+  const unsigned t0 = (unsigned)clock();
+  while (!mbar_try_wait(bar, parity))
+    if ((unsigned)clock() - t0 > limit) {
+      atomicOr(&g_err_lin, kErrTimeout);
+      return false;
+    }
+  return true;
+}
+// ... by a whole warp: all of its lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned limit) {
+  return __all_sync(0xffffffffu, one_wait(bar, parity, limit));
+}
+
 struct Params {
   hymba_linear_attention a;
   int blocks;      // dv blocks of 64 * NV columns
-  long long wlim;
+  unsigned wlim;   // bounded waits: SM clock cycles
 };
 
 template <int NK, int NV>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmZ,
+                        const __grid_constant__ CUtensorMap tmO,
                         const __grid_constant__ Params prm) {
   pdl_wait();
   pdl_trigger();
@@ -79,14 +104,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *o_full = bars + 12, *o_empty = bars + 13;      // outputs ready / read
   uint64_t *k_full = bars + 14, *c_full = bars + 15;       // weighted keys / chunk's state ready
   uint64_t *sb_full = bars + 16, *qs_done = bars + 17;     // state operand ready / read
-  uint64_t *drain = bars + 18;
+  uint64_t *o_staged = bars + 18;                          // output rows staged
+  uint64_t *drain = bars + 19;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 20);
   Decays *dec = reinterpret_cast<Decays *>(smem + Lay::DEC);
   float *s_skip = reinterpret_cast<float *>(smem + Lay::SKIP);
 
   const hymba_linear_attention &a = prm.a;
   const int warp = warp_id(), lane = lane_id();
-  const long long wlim = prm.wlim;
+  const unsigned wlim = prm.wlim;
   const int blk = blockIdx.x % prm.blocks;
   const int bh = blockIdx.x / prm.blocks;
   const int h = bh % a.n_heads, b = bh / a.n_heads;
@@ -94,18 +120,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int p0 = blk * 64 * NV;                    // first state row (column of v and o)
   const int pn = min(64 * NV, a.dv - p0);          // and how many
   const int len = linear_length(a, b);
-  const int chunks = (len + C - 1) / C;
   const int ksteps = (a.dk + 15) / 16;
 
   if (warp == 0 && lane == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&full[x], 1);
-      mbar_init(&empty[x], 1 + 4);  // products retired, epilogue's four warps
+      mbar_init(&empty[x], 1 + 1);  // products retired, V read or the output staged over it stored
       mbar_init(&dec_full[x], 1);
-      mbar_init(&dec_empty[x], 8);
+      mbar_init(&dec_empty[x], 12);
     }
     mbar_init(z_full, 1);
-    mbar_init(z_empty, 4);
+    mbar_init(z_empty, 1);
     mbar_init(s_full, 1);
     mbar_init(p_full, 4);
     mbar_init(o_full, 1);
@@ -114,8 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(c_full, 1);
     mbar_init(sb_full, 128);
     mbar_init(qs_done, 1);
+    mbar_init(o_staged, 4);
     mbar_init(drain, 1);
     fence_barrier_init();
+    tmem_slot[1] = *reinterpret_cast<volatile unsigned *>(&g_err_lin);
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -129,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = tmem_slot[0];
+  const bool failed = tmem_slot[1] != 0u;
+  const int chunks = failed ? 0 : (len + C - 1) / C;
   const uint32_t tS = tmem, tO = tmem + 128, tX = tmem + 256, tC = tmem + 384;
 
   if (warp < 4) {
@@ -142,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; c < chunks; ++c) {
           const int st = c % ST;
           const uint32_t ph = uint32_t(c / ST) & 1u;
-          if (!mbar_wait(&empty[st], ph ^ 1u, &g_err_lin, wlim)) { ok = false; break; }
+          if (!one_wait(&empty[st], ph ^ 1u, wlim)) { ok = false; break; }
           uint8_t *dst = smem + st * Lay::STAGE;
           mbar_arrive_expect_tx(&full[st], Lay::STAGE);
           for (int x = 0; x < NK; ++x) {
@@ -151,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (int x = 0; x < NV; ++x)
             tma_load_4d(dst + Lay::V + x * kAtom, &tmV, &full[st], p0 + 64 * x, h, c * C, b);
-          if (Lay::GATE && a.gate) {
-            if (!mbar_wait(z_empty, (uint32_t(c) & 1u) ^ 1u, &g_err_lin, wlim)) { ok = false; ++c; break; }
+          if (Lay::TILE && a.gate) {
+            if (!one_wait(z_empty, (uint32_t(c) & 1u) ^ 1u, wlim)) { ok = false; ++c; break; }
             mbar_arrive_expect_tx(z_full, NV * kAtom);
             for (int x = 0; x < NV; ++x)
               tma_load_4d(smem + Lay::Z + x * kAtom, &tmZ, z_full, p0 + 64 * x, h, c * C, b);
@@ -172,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idS = make_idesc(C, 1, 0, 0);
         constexpr uint32_t idPV = make_idesc(64 * NV, 1, 0, 1);
         constexpr uint32_t idQS = make_idesc(64 * NV, 1, 0, 0);
-        const uint32_t idC = make_idesc(16 * ksteps, 1, 1, 1);
+        const uint32_t idC = make_idesc(NK == 1 ? 128 : 16 * ksteps, 1, 1, 1);
+        constexpr uint32_t idCl = make_idesc(64, 1, 1, 1);
         const uint32_t mid = smem_u32(smem + Lay::MID), sb = smem_u32(smem + Lay::SB);
         for (int c = 0; c < chunks; ++c) {
           const int st = c % ST;
@@ -182,39 +212,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t v = smem_u32(smem + st * Lay::STAGE + Lay::V);
           const int jsteps = (min(C, len - c * C) + 15) / 16;  // 16-row steps that hold rows
           // scores (their columns were last read by the previous chunk's P V, in order)
-          if (!mbar_wait(&full[st], uint32_t(c / ST) & 1u, &g_err_lin, wlim)) break;
+          if (!one_wait(&full[st], uint32_t(c / ST) & 1u, wlim)) break;
           tc_fence_after();
+#pragma unroll 1
           for (int x = 0; x < ksteps; ++x) {
             const uint32_t off = (x >> 2) * kAtom + (x & 3) * 32;
             mma_bf16_ss(tS, make_sdesc(q + off, 16, 1024), make_sdesc(k + off, 16, 1024), idS, x > 0);
           }
           mma_commit(s_full);
           // Q S^T: high part, then low part
-          if (!mbar_wait(sb_full, ph, &g_err_lin, wlim) || !mbar_wait(o_empty, ph ^ 1u, &g_err_lin, wlim)) break;
+          if (!one_wait(sb_full, ph, wlim) || !one_wait(o_empty, ph ^ 1u, wlim)) break;
           tc_fence_after();
+#pragma unroll 1
           for (int part = 0; part < 2; ++part)
+#pragma unroll 1
             for (int x = 0; x < ksteps; ++x) {
               const uint32_t soff = part * Lay::SB_PART + (x >> 2) * (NV * kAtom / 2) + (x & 3) * 32;
               mma_bf16_ss(tX, make_sdesc(q + (x >> 2) * kAtom + (x & 3) * 32, 16, 1024),
                           make_sdesc(sb + soff, 16, 1024), idQS, part > 0 || x > 0);
             }
           mma_commit(qs_done);
-          // V^T K': high parts (over the keys), middle parts, low parts (over the queries)
-          if (!mbar_wait(k_full, ph, &g_err_lin, wlim)) break;
+          // P V; in a chunk that ends early only once the rows behind the sequence are zero
+          if (a.lengths && len - c * C < C && !one_wait(k_full, ph, wlim)) break;
+          if (!one_wait(p_full, ph, wlim)) break;
           tc_fence_after();
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t kp = part == 0 ? k : part == 1 ? mid : q;
-            for (int x = 0; x < jsteps; ++x)
-              mma_bf16_ss(tC, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(kp + x * 2048, kAtom, 1024), idC,
-                          part > 0 || x > 0);
-          }
-          mma_commit(c_full);
-          // P V
-          if (!mbar_wait(p_full, ph, &g_err_lin, wlim)) break;
-          tc_fence_after();
+#pragma unroll 1
           for (int x = 0; x < jsteps; ++x)
             mma_bf16_ts(tO, tS + 8 * x, make_sdesc(v + x * 2048, kAtom, 1024), idPV, x > 0);
           mma_commit(o_full);
+          // V^T K': high parts (over the keys), middle parts, low parts (over the queries); with
+          // dk <= 64 the first two at once, as 64 columns each of one operand, and the low parts
+          // added to the middle ones
+          if (!one_wait(k_full, ph, wlim)) break;
+          tc_fence_after();
+          if constexpr (NK == 1) {
+#pragma unroll 1
+            for (int x = 0; x < jsteps; ++x)
+              mma_bf16_ss(tC, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(k + x * 2048, mid - k, 1024), idC, x > 0);
+#pragma unroll 1
+            for (int x = 0; x < jsteps; ++x)
+              mma_bf16_ss(tC + 64, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(q + x * 2048, kAtom, 1024), idCl, 1);
+          } else {
+#pragma unroll 1
+            for (int part = 0; part < 3; ++part) {
+              const uint32_t kp = part == 0 ? k : part == 1 ? mid : q;
+#pragma unroll 1
+              for (int x = 0; x < jsteps; ++x)
+                mma_bf16_ss(tC, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(kp + x * 2048, kAtom, 1024), idC,
+                            part > 0 || x > 0);
+            }
+          }
+          mma_commit(c_full);
           mma_commit(&empty[st]);
         }
         // the products in flight end before tensor memory is released
@@ -258,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) G[i] += before;
         const double end = __shfl_sync(0xffffffffu, G[3], 31);
         const double blk_end = __shfl_sync(0xffffffffu, G[3], lane | 7);
-        if (!mbar_wait(&dec_empty[c & 1], (uint32_t(c >> 1) & 1u) ^ 1u, &g_err_lin, wlim)) break;
+        if (!warp_wait(&dec_empty[c & 1], (uint32_t(c >> 1) & 1u) ^ 1u, wlim)) break;
         Decays &d = dec[c & 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -276,19 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegWork));
-    // ---------------- scores and output: one row of the chunk per thread ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegScores));
+    // ---------------- scores: one row of the chunk per thread ----------------
     const int w = warp - 4, r = 32 * w + lane;
     const uint32_t lanes = uint32_t(32 * w) << 16;
-    __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o) + b * a.o_batch + h * a.o_head + p0;
-    const __nv_bfloat16 *zp =
-        reinterpret_cast<const __nv_bfloat16 *>(a.gate) + (a.gate ? b * a.gate_batch + h * a.gate_head + p0 : 0);
     for (int c = 0; c < chunks; ++c) {
       const uint32_t ph = uint32_t(c) & 1u;
       const Decays &d = dec[c & 1];
-      if (!mbar_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, &g_err_lin, wlim)) break;
-      const float hi = d.hi[r], lo = d.lo[r], e = d.e[r];
-      if (!mbar_wait(s_full, ph, &g_err_lin, wlim)) break;
+      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
+      const float hi = d.hi[r], lo = d.lo[r];
+      if (!warp_wait(s_full, ph, wlim)) break;
       tc_fence_after();
       // Row r of warp w sees the whole blocks of 32 columns before block w, the part of its
       // own block up to its diagonal, and nothing behind.  A whole block's factors split at
@@ -305,36 +350,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tS + lanes + 32 * J, sc);
           tmem_wait_ld();
           if (J < w) {
-            const float f = ex2_ftz((hi - d.hi[32 * J + 31]) + (lo - d.lo[32 * J + 31]));
-            const float2 f2 = make_float2(f, f);
+          const float f = ex2_ftz((hi - d.hi[32 * J + 31]) + (lo - d.lo[32 * J + 31]));
+          const float2 f2 = make_float2(f, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 cj = *reinterpret_cast<const float4 *>(&d.c[32 * J + 4 * i]);
-              const float2 x = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i]), __uint_as_float(sc[4 * i + 1])), f2),
-                                     make_float2(cj.x, cj.y));
-              const float2 y = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i + 2]), __uint_as_float(sc[4 * i + 3])), f2),
-                                     make_float2(cj.z, cj.w));
-              pk[2 * i] = pack_bf16x2(x.x, x.y);
-              pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 h4 = *reinterpret_cast<const float4 *>(&d.hi[32 * J + 4 * i]);
-              const float4 l4 = *reinterpret_cast<const float4 *>(&d.lo[32 * J + 4 * i]);
-              const float4 s4 = *reinterpret_cast<const float4 *>(&d.s[32 * J + 4 * i]);
-              const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
-              const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
-              float x[4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-                x[m] = 4 * i + m <= lane
-                           ? __uint_as_float(sc[4 * i + m]) * (sj[m] * ex2_ftz((hi - hj[m]) + (lo - lj[m])))
-                           : 0.f;
-              pk[2 * i] = pack_bf16x2(x[0], x[1]);
-              pk[2 * i + 1] = pack_bf16x2(x[2], x[3]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float4 cj = *reinterpret_cast<const float4 *>(&d.c[32 * J + 4 * i]);
+            const float2 x = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i]), __uint_as_float(sc[4 * i + 1])), f2),
+                                   make_float2(cj.x, cj.y));
+            const float2 y = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i + 2]), __uint_as_float(sc[4 * i + 3])), f2),
+                                   make_float2(cj.z, cj.w));
+            pk[2 * i] = pack_bf16x2(x.x, x.y);
+            pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 h4 = *reinterpret_cast<const float4 *>(&d.hi[32 * J + 4 * i]);
+            const float4 l4 = *reinterpret_cast<const float4 *>(&d.lo[32 * J + 4 * i]);
+            const float4 s4 = *reinterpret_cast<const float4 *>(&d.s[32 * J + 4 * i]);
+            const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+            const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
+            float x[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              x[m] = 4 * i + m <= lane
+                         ? __uint_as_float(sc[4 * i + m]) * (sj[m] * ex2_ftz((hi - hj[m]) + (lo - lj[m])))
+                         : 0.f;
+            pk[2 * i] = pack_bf16x2(x[0], x[1]);
+            pk[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+          }
+        }
         }
         // P over score columns that this row has read already
         tmem_st16(tS + lanes + 16 * J, pk);
@@ -346,13 +391,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_full);
         mbar_arrive(&dec_empty[c & 1]);
       }
-      // output
+    }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegOut));
+    // ---------------- output: one row of the chunk per thread ----------------
+    const int w = warp - 12, r = 32 * w + lane;
+    const uint32_t lanes = uint32_t(32 * w) << 16;
+    __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o) + b * a.o_batch + h * a.o_head + p0;
+    const __nv_bfloat16 *zp =
+        reinterpret_cast<const __nv_bfloat16 *>(a.gate) + (a.gate ? b * a.gate_batch + h * a.gate_head + p0 : 0);
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = uint32_t(c) & 1u;
       const int st = c % ST;
       const long long t = (long long)c * C + r;
       const bool live = t < len;
+      // rows behind a sequence's end inside the tensor must stay as they were, which a tile
+      // store would not leave them: such a chunk's rows are stored one by one
+      const bool by_row = a.lengths && len - c * C < C;
+      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
+      const float e = dec[c & 1].e[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
       const uint8_t *vs = smem + st * Lay::STAGE + Lay::V;
-      if (Lay::GATE && a.gate && !mbar_wait(z_full, ph, &g_err_lin, wlim)) break;
-      if (!mbar_wait(o_full, ph, &g_err_lin, wlim)) break;
+      uint8_t *os = Lay::TILE ? smem + Lay::Z : smem + st * Lay::STAGE + Lay::V;
+      // the tile: this chunk's gate, or free of the last chunk's output
+      if (Lay::TILE && !warp_wait(a.gate ? z_full : z_empty, a.gate ? ph : ph ^ 1u, wlim)) break;
+      if (!warp_wait(o_full, ph, wlim)) break;
+      if (!Lay::TILE && !warp_wait(c_full, ph, wlim)) break;  // V has been read
       tc_fence_after();
       const float2 e2 = make_float2(e, e), sc2 = make_float2(a.scale, a.scale);
 #pragma unroll 1
@@ -386,34 +451,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             y[2] = ffma2(make_float2(k1.x, k1.y), make_float2(bf16_lo(vv.z), bf16_hi(vv.z)), y[2]);
             y[3] = ffma2(make_float2(k1.z, k1.w), make_float2(bf16_lo(vv.w), bf16_hi(vv.w)), y[3]);
           }
-          if (live && col < pn) {
-            if (a.gate) {
-              const uint4 zz = Lay::GATE ? *reinterpret_cast<const uint4 *>(smem + Lay::Z + off)
-                                         : __ldg(reinterpret_cast<const uint4 *>(zp + t * a.gate_row + col));
-              y[0] = fmul2(y[0], make_float2(bf16_lo(zz.x), bf16_hi(zz.x)));
-              y[1] = fmul2(y[1], make_float2(bf16_lo(zz.y), bf16_hi(zz.y)));
-              y[2] = fmul2(y[2], make_float2(bf16_lo(zz.z), bf16_hi(zz.z)));
-              y[3] = fmul2(y[3], make_float2(bf16_lo(zz.w), bf16_hi(zz.w)));
-            }
-            st_global_v4(op + t * a.o_row + col, pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
-                         pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+          if (a.gate) {
+            uint4 zz = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (Lay::TILE) zz = *reinterpret_cast<const uint4 *>(os + off);
+            else if (live && col < pn) zz = __ldg(reinterpret_cast<const uint4 *>(zp + t * a.gate_row + col));
+            y[0] = fmul2(y[0], make_float2(bf16_lo(zz.x), bf16_hi(zz.x)));
+            y[1] = fmul2(y[1], make_float2(bf16_lo(zz.y), bf16_hi(zz.y)));
+            y[2] = fmul2(y[2], make_float2(bf16_lo(zz.z), bf16_hi(zz.z)));
+            y[3] = fmul2(y[3], make_float2(bf16_lo(zz.w), bf16_hi(zz.w)));
           }
+          const uint4 out = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                                       pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+          if (!by_row) *reinterpret_cast<uint4 *>(os + off) = out;
+          else if (live && col < pn) st_global_v4(op + t * a.o_row + col, out.x, out.y, out.z, out.w);
         }
       }
+      fence_proxy_async();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&empty[st]);
-        mbar_arrive(z_empty);
+      if (lane == 0) mbar_arrive(o_staged);
+      if (w == 0 && lane == 0 && one_wait(o_staged, ph, wlim)) {  // every row staged, V read
+        if (Lay::TILE) mbar_arrive(&empty[st]);
+        if (!by_row) {
+          for (int x = 0; x < NV; ++x)
+            if (64 * x < pn) tma_store_4d(&tmO, os + x * kAtom, p0 + 64 * x, h, c * C, b);
+          bulk_commit();
+          bulk_wait_read();
+        }
+        mbar_arrive(Lay::TILE ? z_empty : &empty[st]);
       }
     }
+    if (w == 0 && lane == 0) bulk_wait_all();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegWork));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegState));
     // ---------------- state: row r of the chunk's keys, row r of the state block ----------------
     const int w = warp - 8, r = 32 * w + lane;
     const uint32_t lanes = uint32_t(32 * w) << 16;
     const long long dense = (long long)a.dv * a.dk;
     const bool mine = r < pn;
-    constexpr bool kKeepLow = NK == 1;  // the low parts wait for Q S^T in registers, where they fit
     float S[64 * NK];
     {
       const float *src = a.state_in + (a.state_in ? b * a.state_in_batch + h * dense + (long long)(p0 + r) * a.dk : 0);
@@ -433,9 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = S[n + 2 * i], y = S[n + 2 * i + 1];
-            hi[i] = pack_bf16x2(x, y);
-            lo[i] = pack_bf16x2(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+            const float2 x = make_float2(S[n + 2 * i], S[n + 2 * i + 1]);
+            hi[i] = high_pair(x);
+            const float2 y = fsub2(x, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
+            lo[i] = pack_bf16x2(y.x, y.y);
           }
           const uint32_t off = (n >> 6) * (NV * kAtom / 2) + ((((n & 63) >> 3) ^ (r & 7)) << 4);
           *reinterpret_cast<uint4 *>(sb + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -445,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async();
       mbar_arrive(sb_full);
     };
-    bool ok = true;
+    bool ok = !failed;
     if (chunks > 0) write_state();
     for (int c = 0; c < chunks; ++c) {
       const int st = c % ST;
@@ -453,68 +528,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rem = len - c * C;
       const Decays &d = dec[c & 1];
       // weighted keys, split over three buffers whose operands have been read: the high parts
-      // over the keys (behind the scores), the middle parts beside them, the low parts over
-      // the queries (behind Q S^T)
-      if (!mbar_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, &g_err_lin, wlim) ||
-          !mbar_wait(&full[st], uint32_t(c / ST) & 1u, &g_err_lin, wlim) || !mbar_wait(s_full, ph, &g_err_lin, wlim) ||
-          (!kKeepLow && !mbar_wait(qs_done, ph, &g_err_lin, wlim))) {
+      // over the keys, the middle parts beside them, the low parts over the queries (the
+      // scores and Q S^T are behind)
+      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim) ||
+          !warp_wait(&full[st], uint32_t(c / ST) & 1u, wlim) || !warp_wait(qs_done, ph, wlim)) {
         ok = false;
         break;
       }
       const float wj = d.w[r], decay = d.e[C - 1];
       uint8_t *krow = smem + st * Lay::STAGE + Lay::K + r * 128, *mrow = smem + Lay::MID + r * 128;
       uint8_t *qrow = smem + st * Lay::STAGE + Lay::Q + r * 128;
-      uint32_t low[kKeepLow ? 32 * NK : 1];
-#pragma unroll
+#pragma unroll 2
       for (int x = 0; x < 8 * NK; ++x) {
         const uint32_t off = (x >> 3) * kAtom + (((x & 7) ^ (r & 7)) << 4);
-        const uint4 kk = *reinterpret_cast<const uint4 *>(krow + off);
+        uint4 kk = *reinterpret_cast<const uint4 *>(krow + off);
+        if (r >= rem) kk = make_uint4(0u, 0u, 0u, 0u);  // rows behind the sequence, whatever they hold
         const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
         uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float2 y = fmul2(make_float2(wj, wj), make_float2(bf16_lo(in[i]), bf16_hi(in[i])));
-          if (r >= rem) y = make_float2(0.f, 0.f);  // rows behind the sequence, whatever they hold
-          hi[i] = pack_bf16x2(y.x, y.y);
+          hi[i] = high_pair(y);
           y = fsub2(y, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
-          mid[i] = pack_bf16x2(y.x, y.y);
+          mid[i] = high_pair(y);
           y = fsub2(y, make_float2(bf16_lo(mid[i]), bf16_hi(mid[i])));
-          lo[i] = pack_bf16x2(y.x, y.y);
-          if constexpr (kKeepLow) low[4 * x + i] = lo[i];
+          lo[i] = high_pair(y);
         }
         *reinterpret_cast<uint4 *>(krow + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(mrow + off) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-        if constexpr (!kKeepLow) *reinterpret_cast<uint4 *>(qrow + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4 *>(qrow + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       if (r >= rem) {  // 0 * v must be 0 in the products
         uint8_t *vrow = smem + st * Lay::STAGE + Lay::V + r * 128;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 8 * NV; ++x)
           *reinterpret_cast<uint4 *>(vrow + (x >> 3) * kAtom + ((x & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      if constexpr (kKeepLow) {
-        if (!mbar_wait(qs_done, ph, &g_err_lin, wlim)) { ok = false; break; }
-#pragma unroll
-        for (int x = 0; x < 8 * NK; ++x)
-          *reinterpret_cast<uint4 *>(qrow + (x >> 3) * kAtom + (((x & 7) ^ (r & 7)) << 4)) =
-              make_uint4(low[4 * x], low[4 * x + 1], low[4 * x + 2], low[4 * x + 3]);
       }
       fence_proxy_async();
       mbar_arrive(k_full);
       __syncwarp();
       if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
       // the chunk's contribution
-      if (!mbar_wait(c_full, ph, &g_err_lin, wlim)) { ok = false; break; }
+      if (!warp_wait(c_full, ph, wlim)) { ok = false; break; }
       tc_fence_after();
 #pragma unroll
       for (int n = 0; n < 64 * NK; n += 32) {
         if (n < 16 * ksteps) {
-          uint32_t x[32];
+          uint32_t x[32], y[32];
           tmem_ld32(tC + lanes + n, x);
+          if constexpr (NK == 1) tmem_ld32(tC + lanes + 64 + n, y);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (n + i < 16 * ksteps) S[n + i] = fmaf(decay, S[n + i], __uint_as_float(x[i]));
+            if (n + i < 16 * ksteps) {
+              const float add = NK == 1 ? __uint_as_float(x[i]) + __uint_as_float(y[i]) : __uint_as_float(x[i]);
+              S[n + i] = fmaf(decay, S[n + i], add);
+            }
         }
       }
       tc_fence_before();
@@ -563,10 +632,11 @@ hymba_status chunk_launch(const hymba_linear_attention &a, cudaStream_t s) {
     }
     attr_set.mark(dev);
   }
-  CUtensorMap tq, tk, tv, tz;
+  CUtensorMap tq, tk, tv, tz, to;
   if (!head_map(&tq, a.q, a.batch, a.n_rows, a.n_qk_heads, a.dk, a.q_batch, a.q_row, a.q_head) ||
       !head_map(&tk, a.k, a.batch, a.n_rows, a.n_qk_heads, a.dk, a.k_batch, a.k_row, a.k_head) ||
-      !head_map(&tv, a.v, a.batch, a.n_rows, a.n_heads, a.dv, a.v_batch, a.v_row, a.v_head))
+      !head_map(&tv, a.v, a.batch, a.n_rows, a.n_heads, a.dv, a.v_batch, a.v_row, a.v_head) ||
+      !head_map(&to, a.o, a.batch, a.n_rows, a.n_heads, a.dv, a.o_batch, a.o_row, a.o_head))
     return HYMBA_ERR_CUDA;
   tz = tv;
   if (a.gate && !head_map(&tz, a.gate, a.batch, a.n_rows, a.n_heads, a.dv, a.gate_batch, a.gate_row, a.gate_head))
@@ -574,13 +644,15 @@ hymba_status chunk_launch(const hymba_linear_attention &a, cudaStream_t s) {
   Params p{};
   p.a = a;
   p.blocks = (a.dv + 64 * NV - 1) / (64 * NV);
-  p.wlim = wait_limit_cycles();
+  const long long cycles = wait_limit_cycles();
+  p.wlim = cycles > 0x7fffffffLL ? 0x7fffffffu : (unsigned)cycles;
   const long long grid = (long long)a.batch * a.n_heads * p.blocks;
   if (grid > 0x7fffffffLL) {
     set_error("too many sequences and heads");
     return HYMBA_ERR_UNSUPPORTED;
   }
-  launch_kernel(linear_chunk_kernel<NK, NV>, dim3((unsigned)grid), dim3(kThreads), (size_t)Lay::TOTAL, s, tq, tk, tv, tz, p);
+  launch_kernel(linear_chunk_kernel<NK, NV>, dim3((unsigned)grid), dim3(kThreads), (size_t)Lay::TOTAL, s, tq, tk, tv, tz, to,
+                p);
   note_launch(1);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
