@@ -303,8 +303,18 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s);
 hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s);
 // Whole sequences; workspace of linear_attention_workspace_bytes(a) bytes.
 hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s);
+// The rows of few heads split into segments: pass 0 computes each segment's own state (from
+// zero, the first from the call's) and the sum of its log decays, all but the last one's;
+// pass 1 the outputs, each segment from the states before it.  n = 1: pass 1 alone.
+struct LinearSegments {
+  int n, rows;    // segments of `rows` rows
+  int pass;
+  float *state;   // [n, batch * n_heads, dv, dk]; the last slot holds a copy of the call's state
+  double *decay;  // [n, batch * n_heads] log2 of the segments' decays
+};
 // ... of bf16 storage on the tensor cores.
-hymba_status linear_attention_tc(const hymba_linear_attention &a, cudaStream_t s);
+LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a);
+hymba_status linear_attention_tc(const hymba_linear_attention &a, const LinearSegments &seg, cudaStream_t s);
 size_t linear_attention_workspace_bytes(const hymba_linear_attention &a);
 // A rotation's own numbers, for heads of `width` elements.
 hymba_status check_rope(const hymba_rope &r, int width);

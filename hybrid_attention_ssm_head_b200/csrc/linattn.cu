@@ -1,6 +1,8 @@
 // Linear attention with a decay for each head, on the CUDA cores (hymba_linear_attention_*):
 //   S_t = exp(g_t) S_{t-1} + s_t v_t k_t^T,   o_t = (scale S_t q_t + skip v_t) gate_t
 // The state S [dv, dk] is fp32 throughout.
+#include <algorithm>
+
 #include "common.cuh"
 #include "linattn.cuh"
 
@@ -110,7 +112,7 @@ constexpr int kScanState = 64;  // state rows per CTA (two per thread group)
 // so far is carried in fp64, and the next group's first decay takes it up.
 template <typename T, int NC, int CL>
 __global__ void __launch_bounds__(kScanState / 2 * CL)
-    linear_scan_kernel(const __grid_constant__ hymba_linear_attention a) {
+    linear_scan_kernel(const __grid_constant__ hymba_linear_attention a, const __grid_constant__ LinearSegments g) {
   pdl_wait();
   pdl_trigger();
   constexpr int THR = kScanState / 2 * CL, DK = NC * CL;
@@ -118,14 +120,16 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
   __shared__ __align__(16) float s_q[kScanRows][DK], s_k[kScanRows][DK];
   __shared__ __align__(8) float s_v[kScanRows][kScanState], s_z[kScanRows][kScanState];
   __shared__ float2 s_dx[kScanRows];  // (decay, input scale)
-  const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int blocks = (a.dv + kScanState - 1) / kScanState;
+  const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, seg = blockIdx.x / blocks;
   const int hk = h / (a.n_heads / a.n_qk_heads);
-  const int pb = blockIdx.x * kScanState;              // the CTA's first state row
+  const int pb = (blockIdx.x % blocks) * kScanState;   // the CTA's first state row
   const int pn = min(kScanState, a.dv - pb);           // and how many (even)
   const int pr = 2 * (tid / CL), c0 = (tid % CL) * NC; // this thread's row pair and columns
   const bool rows_live = pr < pn;
-  const int L = linear_length(a, b);
-  const long long dense = (long long)a.dv * a.dk;
+  const bool outputs = g.pass == 1;                    // else the segment's state alone
+  const int L = min(linear_length(a, b), (seg + 1) * g.rows);
+  const long long dense = (long long)a.dv * a.dk, heads = (long long)a.batch * a.n_heads, bh = (long long)b * a.n_heads + h;
   const T *qp = reinterpret_cast<const T *>(a.q) + b * a.q_batch + hk * a.q_head;
   const T *kp = reinterpret_cast<const T *>(a.k) + b * a.k_batch + hk * a.k_head;
   const T *vp = reinterpret_cast<const T *>(a.v) + b * a.v_batch + h * a.v_head + pb;
@@ -138,26 +142,53 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int c = 0; c < NC; c += 4) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.state_in && rows_live && c0 + c < a.dk)
-        x = *reinterpret_cast<const float4 *>(a.state_in + b * a.state_in_batch + h * dense +
-                                              (long long)(pb + pr + r) * a.dk + c0 + c);
-      S[r][c / 2] = make_float2(x.x, x.y);
-      S[r][c / 2 + 1] = make_float2(x.z, x.w);
-    }
+    for (int c = 0; c < NC / 2; ++c) S[r][c] = make_float2(0.f, 0.f);
+  // The state the segment starts from: the call's, or the earlier segments' own states, each
+  // decayed by those after it (a segment's own state starts from zero, the first one's from
+  // the call's).
+  const float *from = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
+  if (outputs && g.n > 1) from = a.state_in ? g.state + ((g.n - 1) * heads + bh) * dense : nullptr;
+  const int first = outputs ? 0 : seg;
+  for (int j = first; j <= seg; ++j) {
+    const float *src = j > first ? g.state + ((j - 1) * heads + bh) * dense : seg == 0 ? from : nullptr;
+    if (!src || !rows_live) continue;
+    const float keep = j > first ? exp2f((float)g.decay[(j - 1) * heads + bh]) : 0.f;
+    const float2 k2 = make_float2(keep, keep);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < NC; c += 4)
+        if (c0 + c < a.dk) {
+          const float4 x = *reinterpret_cast<const float4 *>(src + (long long)(pb + pr + r) * a.dk + c0 + c);
+          S[r][c / 2] = ffma2(k2, S[r][c / 2], make_float2(x.x, x.y));
+          S[r][c / 2 + 1] = ffma2(k2, S[r][c / 2 + 1], make_float2(x.z, x.w));
+        }
+  }
+  auto store_state = [&](float *dst) {
+    if (!rows_live) return;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < NC; c += 4)
+        if (c0 + c < a.dk)
+          *reinterpret_cast<float4 *>(dst + (long long)(pb + pr + r) * a.dk + c0 + c) =
+              make_float4(S[r][c / 2].x, S[r][c / 2].y, S[r][c / 2 + 1].x, S[r][c / 2 + 1].y);
+  };
+  if (!outputs && seg == 0 && a.state_in)  // a copy for the outputs' pass, which may write in place
+    store_state(g.state + ((g.n - 1) * heads + bh) * dense);
   float2 skip = make_float2(0.f, 0.f);
   if (a.skip && rows_live) skip = *reinterpret_cast<const float2 *>(a.skip + (long long)h * a.dv + pb + pr);
 
   double carry = 1.0;  // exp(sum g) over the product of the decays used so far
-  for (int t0 = 0; t0 < L; t0 += kScanRows) {
+  double total = 0.0;  // log2 of this lane's rows' decays
+  for (int t0 = seg * g.rows; t0 < L; t0 += kScanRows) {
     const int nt = min(kScanRows, L - t0);
     __syncthreads();
     for (int i = tid; i < nt * (DK / 4); i += THR) {
       const int t = i / (DK / 4), c = 4 * (i % (DK / 4));
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (c < a.dk) {
-        x = load4(qp + (t0 + t) * a.q_row + c);
+        if (outputs) x = load4(qp + (t0 + t) * a.q_row + c);
         y = load4(kp + (t0 + t) * a.k_row + c);
       }
       *reinterpret_cast<float4 *>(&s_q[t][c]) = x;
@@ -167,13 +198,17 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
       const int t = i / (kScanState / 4), c = 4 * (i % (kScanState / 4));
       if (c < pn) {
         *reinterpret_cast<float4 *>(&s_v[t][c]) = load4(vp + (t0 + t) * a.v_row + c);
-        if (a.gate) *reinterpret_cast<float4 *>(&s_z[t][c]) = load4(zp + (t0 + t) * a.gate_row + c);
+        if (outputs && a.gate) *reinterpret_cast<float4 *>(&s_z[t][c]) = load4(zp + (t0 + t) * a.gate_row + c);
       }
     }
     if (tid < 32) {
       const int t = tid;
       double want = 1.0;
-      if (t < nt && gp) want = linear_decay64(gp[(t0 + t) * a.decay_row]);
+      if (t < nt && gp) {
+        const float gt = linear_log_decay(gp[(t0 + t) * a.decay_row]);
+        want = exp((double)gt);
+        total += (double)gt * 1.4426950408889634074;
+      }
       float used = (float)want;
       // what the rounding of the other rows of this group of kFix leaves over; then each
       // group's first decay in turn takes up what was left over before it
@@ -220,7 +255,7 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
         y0 += __shfl_xor_sync(0xffffffffu, y0, m);
         y1 += __shfl_xor_sync(0xffffffffu, y1, m);
       }
-      if (tid % CL == 0 && rows_live) {
+      if (outputs && tid % CL == 0 && rows_live) {
         y0 = fmaf(skip.x, v.x, a.scale * y0);
         y1 = fmaf(skip.y, v.y, a.scale * y1);
         if (a.gate) {
@@ -234,15 +269,15 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
       }
     }
   }
-  if (a.state_out && rows_live) {
+  if (!outputs) {
+    if (tid < 32) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int c = 0; c < NC; c += 4)
-        if (c0 + c < a.dk)
-          *reinterpret_cast<float4 *>(a.state_out + ((long long)b * a.n_heads + h) * dense +
-                                      (long long)(pb + pr + r) * a.dk + c0 + c) =
-              make_float4(S[r][c / 2].x, S[r][c / 2].y, S[r][c / 2 + 1].x, S[r][c / 2 + 1].y);
+      for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+      if (tid == 0 && pb == 0) g.decay[seg * heads + bh] = total;
+    }
+    store_state(g.state + (seg * heads + bh) * dense);
+  } else if (a.state_out && seg == g.n - 1) {
+    store_state(a.state_out + bh * dense);
   }
 }
 
@@ -257,13 +292,37 @@ hymba_status launched(const char *what) {
 }
 
 template <typename T>
-void scan_launch(const hymba_linear_attention &a, cudaStream_t s) {
-  const dim3 grid((a.dv + kScanState - 1) / kScanState, a.n_heads, a.batch);
+void scan_launch(const hymba_linear_attention &a, LinearSegments g, cudaStream_t s) {
   constexpr int one = kScanState / 2;
-  if (a.dk <= 16) launch_kernel(linear_scan_kernel<T, 16, 1>, grid, dim3(one), 0, s, a);
-  else if (a.dk <= 32) launch_kernel(linear_scan_kernel<T, 32, 1>, grid, dim3(one), 0, s, a);
-  else if (a.dk <= 64) launch_kernel(linear_scan_kernel<T, 32, 2>, grid, dim3(2 * one), 0, s, a);
-  else launch_kernel(linear_scan_kernel<T, 32, 4>, grid, dim3(4 * one), 0, s, a);
+  for (g.pass = g.n > 1 ? 0 : 1; g.pass < 2; ++g.pass) {
+    const dim3 grid((a.dv + kScanState - 1) / kScanState * (g.pass ? g.n : g.n - 1), a.n_heads, a.batch);
+    if (a.dk <= 16) launch_kernel(linear_scan_kernel<T, 16, 1>, grid, dim3(one), 0, s, a, g);
+    else if (a.dk <= 32) launch_kernel(linear_scan_kernel<T, 32, 1>, grid, dim3(one), 0, s, a, g);
+    else if (a.dk <= 64) launch_kernel(linear_scan_kernel<T, 32, 2>, grid, dim3(2 * one), 0, s, a, g);
+    else launch_kernel(linear_scan_kernel<T, 32, 4>, grid, dim3(4 * one), 0, s, a, g);
+    note_launch(1);
+  }
+}
+
+// Few heads of many rows: segments of at least 32 rows, about eight CTAs for each SM.
+LinearSegments scan_segments(const hymba_linear_attention &a) {
+  LinearSegments g{};
+  const long long ctas = (long long)a.batch * a.n_heads * ((a.dv + kScanState - 1) / kScanState);
+  const long long want = std::max<long long>(1, std::min<long long>(8 * 148 / std::max<long long>(1, ctas), a.n_rows / 32));
+  g.rows = (int)(((a.n_rows + want - 1) / want + kScanRows - 1) / kScanRows * kScanRows);
+  g.n = (a.n_rows + g.rows - 1) / g.rows;
+  return g;
+}
+
+// Below this many rows a bf16 sequence is taken row by row: a chunk costs its 128 rows
+// however many count.
+constexpr int kFewRows = 16;
+bool on_tensor_cores(const hymba_linear_attention &a) { return a.dtype == HYMBA_BF16 && a.n_rows >= kFewRows; }
+LinearSegments segments_of(const hymba_linear_attention &a) {
+  return on_tensor_cores(a) ? linear_attention_tc_segments(a) : scan_segments(a);
+}
+size_t segment_state_bytes(const hymba_linear_attention &a, const LinearSegments &g) {
+  return (size_t)g.n * a.batch * a.n_heads * a.dv * a.dk * 4;
 }
 
 }  // namespace
@@ -288,12 +347,26 @@ hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t
   return launched("linear attention step");
 }
 
-size_t linear_attention_workspace_bytes(const hymba_linear_attention &) { return 0; }
+size_t linear_attention_workspace_bytes(const hymba_linear_attention &a) {
+  const LinearSegments g = segments_of(a);
+  return g.n > 1 ? segment_state_bytes(a, g) + (size_t)g.n * a.batch * a.n_heads * 8 : 0;
+}
 
-hymba_status linear_attention(const hymba_linear_attention &a, void *, cudaStream_t s) {
-  if (a.dtype == HYMBA_BF16) return linear_attention_tc(a, s);
-  scan_launch<float>(a, s);
-  return launched("linear attention");
+hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s) {
+  LinearSegments g = segments_of(a);
+  if (g.n > 1) {
+    g.state = reinterpret_cast<float *>(workspace);
+    g.decay = reinterpret_cast<double *>(reinterpret_cast<char *>(workspace) + segment_state_bytes(a, g));
+  }
+  if (on_tensor_cores(a)) return linear_attention_tc(a, g, s);
+  if (a.dtype == HYMBA_BF16) scan_launch<__nv_bfloat16>(a, g, s);
+  else scan_launch<float>(a, g, s);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("linear attention launch failed: %s", cudaGetErrorString(e));
+    return HYMBA_ERR_CUDA;
+  }
+  return HYMBA_OK;
 }
 
 }  // namespace hymba

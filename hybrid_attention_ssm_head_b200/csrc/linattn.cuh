@@ -12,7 +12,6 @@ namespace hymba {
 constexpr float kMinLogDecay = -110.f;
 __device__ __forceinline__ float linear_log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
 __device__ __forceinline__ float linear_decay(float g) { return expf(linear_log_decay(g)); }
-__device__ __forceinline__ double linear_decay64(float g) { return exp((double)linear_log_decay(g)); }
 
 // Rows of sequence b that count.
 __device__ __forceinline__ int linear_length(const hymba_linear_attention &a, int b) {

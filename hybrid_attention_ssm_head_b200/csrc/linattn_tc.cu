@@ -12,6 +12,8 @@
 // whose errors would stay in the state, in three (24 bits, all of an fp32 product): with two
 // parts the state of 8320 rows was 2.5e-6 off in the 2-norm.  A chunk's contribution is
 // summed in tensor memory from zero and added to the state in fp32 by the CUDA cores.
+#include <algorithm>
+
 #include "linattn.cuh"
 #include "tmap.h"
 
@@ -22,34 +24,42 @@ HYMBA_DEVICE_ERROR_WORD(g_err_lin);
 namespace {
 
 constexpr int C = 128;         // rows per chunk
-constexpr int kThreads = 512;  // TMA, MMA and decay warps (+ one idle), scores, state, output
-constexpr int kRegCtrl = 56, kRegScores = 144, kRegState = 184, kRegOut = 128;
-static_assert(kRegCtrl + kRegScores + kRegState + kRegOut == 4 * 128, "the warpgroups share 512 x 128 registers");
+// Warpgroups: control (TMA, MMA, decays: a warp each), scores, keys, output (two), state.
+constexpr int kThreads = 768;
+// Registers a thread of each takes; launched with 80 each.  The state holds dk fp32 values a
+// thread.
+template <int NK>
+struct Regs {
+  static constexpr int LAUNCH = 80, CTRL = NK == 1 ? 72 : 64, SCORES = NK == 1 ? 80 : 72, KEYS = 56;
+  static constexpr int OUT = NK == 1 ? 80 : 64, STATE = NK == 1 ? 112 : 160;
+  static_assert(CTRL + SCORES + KEYS + 2 * OUT + STATE == 6 * LAUNCH, "the warpgroups share the launch's registers");
+};
 constexpr int kAtom = C * 128;  // bytes of 128 rows x 64 bf16 columns, 128-byte swizzle
 
 struct Decays {  // of one chunk's rows, log2 units
   float hi[C], lo[C];  // G = hi + lo, hi a multiple of 1/8: differences of hi are exact
-  float s[C];          // input scale
-  float c[C];          // s exp(G_end of the row's block of 32 - G)
-  float w[C];          // s exp(G_end of the chunk - G)
-  float e[C];          // exp(G)
+  float s[C];          // scale * input scale
+  float c[C];          // scale * input scale * exp(G_end of the row's block of 32 - G)
+  float w[C];          // input scale * exp(G_end of the chunk - G)
+  float e[C];          // scale * exp(G)
+  float end, pad[3];   // exp(G_end of the chunk)
 };
 
 // NK, NV: 64-column atoms of dk and of the CTA's dv block.  For dk <= 64 two stages of
-// (Q, K, V) tiles fit shared memory, and a tile that the gate is loaded into and the output
-// is stored from.  Wider keys take one stage, stage the output over V and read the gate from
-// global memory.
+// (Q, K, V) tiles and a gate tile fit shared memory.  Wider keys take one stage, and read the
+// gate from global memory.
 template <int NK, int NV>
 struct Layout {
   static constexpr int STAGES = NK == 1 ? 2 : 1;
-  static constexpr bool TILE = NK == 1;
+  static constexpr bool GATE = NK == 1;
   static constexpr int Q = 0, K = NK * kAtom, V = 2 * NK * kAtom, STAGE = (2 * NK + NV) * kAtom;
   static constexpr int MID = STAGES * STAGE;            // middle parts of the weighted keys
   static constexpr int SB = MID + NK * kAtom;           // state operand: hi, then lo
   static constexpr int SB_PART = NK * NV * (kAtom / 2); // 64 NV rows of 128 bytes per dk atom
-  static constexpr int Z = SB + 2 * SB_PART;            // gate and output tile
   // the state product reads 128 state rows whatever dv is: for NV = 1 up to one atom behind V
-  static constexpr int DEC = Z + (TILE ? NV * kAtom : 0);
+  static constexpr int Z = SB + 2 * SB_PART;            // gate tile
+  static constexpr int OUT = Z + (GATE ? NV * kAtom : 0);  // output: 32 rows of 32 bytes per warp
+  static constexpr int DEC = OUT + 8 * 1024;
   static constexpr int SKIP = DEC + 2 * (int)sizeof(Decays);
   static constexpr int BAR = SKIP + NV * 64 * 4;
   static constexpr int TOTAL = BAR + 32 * 8 + 1024;  // + alignment of the base
@@ -80,6 +90,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
 
 struct Params {
   hymba_linear_attention a;
+  LinearSegments seg;
   int blocks;      // dv blocks of 64 * NV columns
   unsigned wlim;   // bounded waits: SM clock cycles
 };
@@ -88,7 +99,6 @@ template <int NK, int NV>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmZ,
-                        const __grid_constant__ CUtensorMap tmO,
                         const __grid_constant__ Params prm) {
   pdl_wait();
   pdl_trigger();
@@ -99,14 +109,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::BAR);
   uint64_t *full = bars + 0, *empty = bars + 2;            // [ST] Q, K, V stages
   uint64_t *dec_full = bars + 4, *dec_empty = bars + 6;    // [2] decays
-  uint64_t *z_full = bars + 8, *z_empty = bars + 9;        // gate tile
   uint64_t *s_full = bars + 10, *p_full = bars + 11;       // scores ready / P written over them
   uint64_t *o_full = bars + 12, *o_empty = bars + 13;      // outputs ready / read
-  uint64_t *k_full = bars + 14, *c_full = bars + 15;       // weighted keys / chunk's state ready
-  uint64_t *sb_full = bars + 16, *qs_done = bars + 17;     // state operand ready / read
-  uint64_t *o_staged = bars + 18;                          // output rows staged
-  uint64_t *drain = bars + 19;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 20);
+  uint64_t *z_full = bars + 8, *z_empty = bars + 9;        // gate tile
+  uint64_t *k_full = bars + 15;                            // weighted keys ready
+  uint64_t *c_full = bars + 18, *c_empty = bars + 19;      // the chunk's state ready / read
+  uint64_t *sb_full = bars + 20, *qs_done = bars + 21;     // state operand ready / Q S^T done
+  uint64_t *drain = bars + 22;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23);
   Decays *dec = reinterpret_cast<Decays *>(smem + Lay::DEC);
   float *s_skip = reinterpret_cast<float *>(smem + Lay::SKIP);
 
@@ -114,32 +124,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_id(), lane = lane_id();
   const unsigned wlim = prm.wlim;
   const int blk = blockIdx.x % prm.blocks;
-  const int bh = blockIdx.x / prm.blocks;
+  const int bhs = blockIdx.x / prm.blocks;
+  const int bh = bhs % (a.batch * a.n_heads), seg = bhs / (a.batch * a.n_heads);
   const int h = bh % a.n_heads, b = bh / a.n_heads;
   const int hk = h / (a.n_heads / a.n_qk_heads);
   const int p0 = blk * 64 * NV;                    // first state row (column of v and o)
   const int pn = min(64 * NV, a.dv - p0);          // and how many
-  const int len = linear_length(a, b);
+  const int base = seg * prm.seg.rows;             // the segment's first row
+  const int len = max(0, min(linear_length(a, b) - base, prm.seg.rows));  // and how many count
+  const bool outputs = prm.seg.pass == 1;          // else the segment's state alone
   const int ksteps = (a.dk + 15) / 16;
 
   if (warp == 0 && lane == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&full[x], 1);
-      mbar_init(&empty[x], 1 + 1);  // products retired, V read or the output staged over it stored
+      mbar_init(&empty[x], outputs ? 1 + 8 : 1);  // products retired, V read by the output's warps
       mbar_init(&dec_full[x], 1);
-      mbar_init(&dec_empty[x], 12);
+      mbar_init(&dec_empty[x], outputs ? 20 : 8);
     }
-    mbar_init(z_full, 1);
-    mbar_init(z_empty, 1);
     mbar_init(s_full, 1);
+    mbar_init(z_full, 1);
+    mbar_init(z_empty, 8);
     mbar_init(p_full, 4);
     mbar_init(o_full, 1);
-    mbar_init(o_empty, 4);
+    mbar_init(o_empty, 8);
     mbar_init(k_full, 128);
     mbar_init(c_full, 1);
+    mbar_init(c_empty, 4);
     mbar_init(sb_full, 128);
     mbar_init(qs_done, 1);
-    mbar_init(o_staged, 4);
     mbar_init(drain, 1);
     fence_barrier_init();
     tmem_slot[1] = *reinterpret_cast<volatile unsigned *>(&g_err_lin);
@@ -162,112 +175,110 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS = tmem, tO = tmem + 128, tX = tmem + 256, tC = tmem + 384;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegCtrl));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::CTRL));
     if (warp == 0) {
       if (lane == 0) {
         // ---------------- TMA producer ----------------
         bool ok = true;
-        int c = 0, nz = 0;
+        int c = 0;
         for (; c < chunks; ++c) {
           const int st = c % ST;
           const uint32_t ph = uint32_t(c / ST) & 1u;
           if (!one_wait(&empty[st], ph ^ 1u, wlim)) { ok = false; break; }
           uint8_t *dst = smem + st * Lay::STAGE;
-          mbar_arrive_expect_tx(&full[st], Lay::STAGE);
+          mbar_arrive_expect_tx(&full[st], outputs ? Lay::STAGE : Lay::STAGE - NK * kAtom);
           for (int x = 0; x < NK; ++x) {
-            tma_load_4d(dst + Lay::K + x * kAtom, &tmK, &full[st], 64 * x, hk, c * C, b);
-            tma_load_4d(dst + Lay::Q + x * kAtom, &tmQ, &full[st], 64 * x, hk, c * C, b);
+            tma_load_4d(dst + Lay::K + x * kAtom, &tmK, &full[st], 64 * x, hk, base + c * C, b);
+            if (outputs) tma_load_4d(dst + Lay::Q + x * kAtom, &tmQ, &full[st], 64 * x, hk, base + c * C, b);
           }
           for (int x = 0; x < NV; ++x)
-            tma_load_4d(dst + Lay::V + x * kAtom, &tmV, &full[st], p0 + 64 * x, h, c * C, b);
-          if (Lay::TILE && a.gate) {
-            if (!one_wait(z_empty, (uint32_t(c) & 1u) ^ 1u, wlim)) { ok = false; ++c; break; }
-            mbar_arrive_expect_tx(z_full, NV * kAtom);
-            for (int x = 0; x < NV; ++x)
-              tma_load_4d(smem + Lay::Z + x * kAtom, &tmZ, z_full, p0 + 64 * x, h, c * C, b);
-            ++nz;
-          }
+            tma_load_4d(dst + Lay::V + x * kAtom, &tmV, &full[st], p0 + 64 * x, h, base + c * C, b);
         }
-        if (!ok) {
-          // the copies in flight land before the CTA ends
+        if (!ok)  // the copies in flight land before the CTA ends
           for (int q = c > ST ? c - ST : 0; q < c; ++q)
-            mbar_wait_drain(&full[q % ST], uint32_t(q / ST) & 1u, &g_err_lin, wlim);
-          if (nz) mbar_wait_drain(z_full, uint32_t(nz - 1) & 1u, &g_err_lin, wlim);
-        }
+            one_wait(&full[q % ST], uint32_t(q / ST) & 1u, wlim);
       }
     } else if (warp == 1) {
       if (lane == 0) {
         // ---------------- MMA issuer ----------------
+        // Every loop over a product's 16-wide steps is unrolled, so that each instruction has
+        // descriptor registers of its own: in a rolled loop one instruction's registers are
+        // free for the next only when it has run (390 cycles a step against 80).
         constexpr uint32_t idS = make_idesc(C, 1, 0, 0);
         constexpr uint32_t idPV = make_idesc(64 * NV, 1, 0, 1);
         constexpr uint32_t idQS = make_idesc(64 * NV, 1, 0, 0);
         const uint32_t idC = make_idesc(NK == 1 ? 128 : 16 * ksteps, 1, 1, 1);
         constexpr uint32_t idCl = make_idesc(64, 1, 1, 1);
         const uint32_t mid = smem_u32(smem + Lay::MID), sb = smem_u32(smem + Lay::SB);
-        for (int c = 0; c < chunks; ++c) {
-          const int st = c % ST;
-          const uint32_t ph = uint32_t(c) & 1u;
-          const uint32_t q = smem_u32(smem + st * Lay::STAGE + Lay::Q);
-          const uint32_t k = smem_u32(smem + st * Lay::STAGE + Lay::K);
-          const uint32_t v = smem_u32(smem + st * Lay::STAGE + Lay::V);
-          const int jsteps = (min(C, len - c * C) + 15) / 16;  // 16-row steps that hold rows
-          // scores (their columns were last read by the previous chunk's P V, in order)
-          if (!one_wait(&full[st], uint32_t(c / ST) & 1u, wlim)) break;
+        auto stage = [&](int c, int what) { return smem_u32(smem + (c % ST) * Lay::STAGE + what); };
+        // a step of 16 columns inside a 64-column atom, or of 16 rows, on a descriptor's address
+        auto cols = [](int x, int atom) { return uint64_t(((x >> 2) * atom + (x & 3) * 32) >> 4); };
+        constexpr uint64_t kRows16 = 2048 >> 4;
+        // Q K^T of chunk c: its columns were last read by the P V before it (in order)
+        auto scores = [&](int c) -> bool {
+          if (!one_wait(&full[c % ST], uint32_t(c / ST) & 1u, wlim)) return false;
           tc_fence_after();
-#pragma unroll 1
-          for (int x = 0; x < ksteps; ++x) {
-            const uint32_t off = (x >> 2) * kAtom + (x & 3) * 32;
-            mma_bf16_ss(tS, make_sdesc(q + off, 16, 1024), make_sdesc(k + off, 16, 1024), idS, x > 0);
-          }
+          const uint64_t dq = make_sdesc(stage(c, Lay::Q), 16, 1024), dk = make_sdesc(stage(c, Lay::K), 16, 1024);
+#pragma unroll
+          for (int x = 0; x < 4 * NK; ++x)
+            if (x < ksteps) mma_bf16_ss(tS, dq + cols(x, kAtom), dk + cols(x, kAtom), idS, x > 0);
           mma_commit(s_full);
-          // Q S^T: high part, then low part
-          if (!one_wait(sb_full, ph, wlim) || !one_wait(o_empty, ph ^ 1u, wlim)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part)
-#pragma unroll 1
-            for (int x = 0; x < ksteps; ++x) {
-              const uint32_t soff = part * Lay::SB_PART + (x >> 2) * (NV * kAtom / 2) + (x & 3) * 32;
-              mma_bf16_ss(tX, make_sdesc(q + (x >> 2) * kAtom + (x & 3) * 32, 16, 1024),
-                          make_sdesc(sb + soff, 16, 1024), idQS, part > 0 || x > 0);
-            }
-          mma_commit(qs_done);
-          // P V; in a chunk that ends early only once the rows behind the sequence are zero
-          if (a.lengths && len - c * C < C && !one_wait(k_full, ph, wlim)) break;
-          if (!one_wait(p_full, ph, wlim)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int x = 0; x < jsteps; ++x)
-            mma_bf16_ts(tO, tS + 8 * x, make_sdesc(v + x * 2048, kAtom, 1024), idPV, x > 0);
-          mma_commit(o_full);
+          return true;
+        };
+        bool ok = chunks == 0 || !outputs || scores(0);
+        for (int c = 0; c < chunks && ok; ++c) {
+          ok = false;  // until the end of the chunk
+          const uint32_t ph = uint32_t(c) & 1u;
+          const uint32_t q = stage(c, Lay::Q), k = stage(c, Lay::K);
+          const uint64_t dv = make_sdesc(stage(c, Lay::V), kAtom, 1024);
+          if (outputs) {
+            // Q S^T: high part, then low part
+            if (!one_wait(sb_full, ph, wlim) || !one_wait(o_empty, ph ^ 1u, wlim)) break;
+            tc_fence_after();
+            const uint64_t dq = make_sdesc(q, 16, 1024), ds = make_sdesc(sb, 16, 1024);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int x = 0; x < 4 * NK; ++x)
+                if (x < ksteps)
+                  mma_bf16_ss(tX, dq + cols(x, kAtom), ds + cols(x, NV * kAtom / 2) + part * (Lay::SB_PART >> 4), idQS,
+                              part > 0 || x > 0);
+            mma_commit(qs_done);
+            // in a chunk that ends early P V waits until the rows behind the sequence are zero
+            if (a.lengths && len - c * C < C && !one_wait(k_full, ph, wlim)) break;
+            if (!one_wait(p_full, ph, wlim)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma_bf16_ts(tO, tS + 8 * x, dv + x * kRows16, idPV, x > 0);
+            mma_commit(o_full);
+            // the next chunk's scores, ahead of this one's state, where it has a stage
+            if (ST > 1 && c + 1 < chunks && !scores(c + 1)) break;
+          }
           // V^T K': high parts (over the keys), middle parts, low parts (over the queries); with
           // dk <= 64 the first two at once, as 64 columns each of one operand, and the low parts
           // added to the middle ones
-          if (!one_wait(k_full, ph, wlim)) break;
+          if (!one_wait(k_full, ph, wlim) || !one_wait(c_empty, ph ^ 1u, wlim)) break;
           tc_fence_after();
+          auto state_part = [&](uint64_t dk, uint32_t d, uint32_t id, bool add) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma_bf16_ss(d, dv + x * kRows16, dk + x * kRows16, id, add || x > 0);
+          };
           if constexpr (NK == 1) {
-#pragma unroll 1
-            for (int x = 0; x < jsteps; ++x)
-              mma_bf16_ss(tC, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(k + x * 2048, mid - k, 1024), idC, x > 0);
-#pragma unroll 1
-            for (int x = 0; x < jsteps; ++x)
-              mma_bf16_ss(tC + 64, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(q + x * 2048, kAtom, 1024), idCl, 1);
+            state_part(make_sdesc(k, mid - k, 1024), tC, idC, false);
+            state_part(make_sdesc(q, kAtom, 1024), tC + 64, idCl, true);
           } else {
-#pragma unroll 1
-            for (int part = 0; part < 3; ++part) {
-              const uint32_t kp = part == 0 ? k : part == 1 ? mid : q;
-#pragma unroll 1
-              for (int x = 0; x < jsteps; ++x)
-                mma_bf16_ss(tC, make_sdesc(v + x * 2048, kAtom, 1024), make_sdesc(kp + x * 2048, kAtom, 1024), idC,
-                            part > 0 || x > 0);
-            }
+            state_part(make_sdesc(k, kAtom, 1024), tC, idC, false);
+            state_part(make_sdesc(mid, kAtom, 1024), tC, idC, true);
+            state_part(make_sdesc(q, kAtom, 1024), tC, idC, true);
           }
           mma_commit(c_full);
-          mma_commit(&empty[st]);
+          mma_commit(&empty[c % ST]);
+          if (ST == 1 && outputs && c + 1 < chunks && !scores(c + 1)) break;
+          ok = true;
         }
         // the products in flight end before tensor memory is released
         mma_commit(drain);
-        mbar_wait_drain(drain, 0, &g_err_lin, wlim);
+        one_wait(drain, 0, wlim);
       }
     } else if (warp == 2) {
       // ---------------- decays: lane l takes rows 4 l .. 4 l + 3 of a chunk ----------------
@@ -277,12 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch = [&](int c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const long long t = (long long)c * C + 4 * lane + i;
+          const int t = c * C + 4 * lane + i;
           const bool in = t < len;
-          g[i] = in && gp ? gp[t * a.decay_row] : 0.f;
-          s[i] = in ? (sp ? sp[t * a.scale_row] : 1.f) : 0.f;
+          g[i] = in && gp ? gp[(long long)(base + t) * a.decay_row] : 0.f;
+          s[i] = in ? (sp ? sp[(long long)(base + t) * a.scale_row] : 1.f) : 0.f;
         }
       };
+      double total = 0.0;
       if (chunks > 0) fetch(0);
       for (int c = 0; c < chunks; ++c) {
         double G[4];
@@ -314,21 +326,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float hi = (float)rint(G[i] * 8.0) * 0.125f;
           d.hi[r] = hi;
           d.lo[r] = (float)(G[i] - (double)hi);
-          d.s[r] = si[i];
-          d.c[r] = si[i] * exp2f((float)(blk_end - G[i]));
-          d.w[r] = si[i] * exp2f((float)(end - G[i]));
-          d.e[r] = exp2f((float)G[i]);
+          d.s[r] = a.scale * si[i];
+          d.c[r] = a.scale * si[i] * ex2_ftz((float)(blk_end - G[i]));
+          d.w[r] = si[i] * ex2_ftz((float)(end - G[i]));
+          d.e[r] = a.scale * ex2_ftz((float)G[i]);
         }
+        if (lane == 31) d.end = exp2f((float)end);
+        total += end;
         __syncwarp();
         if (lane == 0) mbar_arrive(&dec_full[c & 1]);
       }
+      if (!outputs && lane == 0 && blk == 0) prm.seg.decay[bhs] = total;  // log2 of the segment's decay
+    } else if (Lay::GATE && a.gate && outputs && lane == 0) {
+      // ---------------- gate producer ----------------
+      bool ok = true;
+      int c = 0;
+      for (; c < chunks; ++c) {
+        if (!one_wait(z_empty, (uint32_t(c) & 1u) ^ 1u, wlim)) { ok = false; break; }
+        mbar_arrive_expect_tx(z_full, NV * kAtom);
+        for (int x = 0; x < NV; ++x)
+          tma_load_4d(smem + Lay::Z + x * kAtom, &tmZ, z_full, p0 + 64 * x, h, base + c * C, b);
+      }
+      if (!ok && c > 0) one_wait(z_full, uint32_t(c - 1) & 1u, wlim);
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegScores));
+    if constexpr (Regs<NK>::SCORES < Regs<NK>::LAUNCH)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::SCORES));
     // ---------------- scores: one row of the chunk per thread ----------------
     const int w = warp - 4, r = 32 * w + lane;
     const uint32_t lanes = uint32_t(32 * w) << 16;
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; outputs && c < chunks; ++c) {
       const uint32_t ph = uint32_t(c) & 1u;
       const Decays &d = dec[c & 1];
       if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
@@ -392,153 +419,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&dec_empty[c & 1]);
       }
     }
-  } else if (warp >= 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegOut));
-    // ---------------- output: one row of the chunk per thread ----------------
-    const int w = warp - 12, r = 32 * w + lane;
-    const uint32_t lanes = uint32_t(32 * w) << 16;
-    __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o) + b * a.o_batch + h * a.o_head + p0;
-    const __nv_bfloat16 *zp =
-        reinterpret_cast<const __nv_bfloat16 *>(a.gate) + (a.gate ? b * a.gate_batch + h * a.gate_head + p0 : 0);
-    for (int c = 0; c < chunks; ++c) {
+  } else if (warp >= 12 && warp < 20) {
+    if constexpr (Regs<NK>::OUT < Regs<NK>::LAUNCH)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::OUT));
+    // ---------------- output: half of the columns of one row of the chunk per thread ----------------
+    constexpr int kCols = 32 * NV;
+    const int w = (warp - 12) & 3, r = 32 * w + lane, first = kCols * ((warp - 12) >> 2);
+    const uint32_t lanes = (uint32_t(32 * w) << 16) + first;
+    const float *skip = s_skip + first;
+    const bool skips = a.skip != nullptr, gates = a.gate != nullptr;
+    // this row's 16-byte pieces of a 128-row tile
+    const uint32_t row = (first >> 6) * kAtom + r * 128, p8 = (first & 63) >> 3, swz = r & 7;
+    // Rows are stored through shared memory 16 columns at a time, so that two lanes write the
+    // 32 contiguous bytes of a sector: this lane rows row0 and row0 + 16, columns half ..
+    const int half = 8 * (lane & 1), row0 = lane >> 1;
+    const int cols = pn - first - half;  // > 16 x: the lane's piece of group x exists
+    uint8_t *stage = smem + Lay::OUT + (warp - 12) * 1024;
+    const uint32_t put = lane * 32 + (((lane >> 2) & 1) << 4);
+    const uint32_t get = row0 * 32 + (((lane & 1) ^ ((row0 >> 2) & 1)) << 4);  // row0 + 16: the same bits
+    char *orow = reinterpret_cast<char *>(a.o) +
+                 2 * (b * a.o_batch + h * a.o_head + (base + 32 * w + row0) * a.o_row + p0 + first + half);
+    const char *zrow = reinterpret_cast<const char *>(a.gate);
+    if (gates) zrow += 2 * (b * a.gate_batch + h * a.gate_head + (base + r) * a.gate_row + p0 + first);
+    for (int c = 0; outputs && c < chunks; ++c) {
       const uint32_t ph = uint32_t(c) & 1u;
       const int st = c % ST;
-      const long long t = (long long)c * C + r;
-      const bool live = t < len;
-      // rows behind a sequence's end inside the tensor must stay as they were, which a tile
-      // store would not leave them: such a chunk's rows are stored one by one
-      const bool by_row = a.lengths && len - c * C < C;
+      const int rows = len - c * C - 32 * w;  // rows of this warp that count (may be none)
       if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
       const float e = dec[c & 1].e[r];
       __syncwarp();
       if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
-      const uint8_t *vs = smem + st * Lay::STAGE + Lay::V;
-      uint8_t *os = Lay::TILE ? smem + Lay::Z : smem + st * Lay::STAGE + Lay::V;
-      // the tile: this chunk's gate, or free of the last chunk's output
-      if (Lay::TILE && !warp_wait(a.gate ? z_full : z_empty, a.gate ? ph : ph ^ 1u, wlim)) break;
+      if (Lay::GATE && gates && !warp_wait(z_full, ph, wlim)) break;
+      const uint8_t *vs = smem + st * Lay::STAGE + Lay::V + row;
       if (!warp_wait(o_full, ph, wlim)) break;
-      if (!Lay::TILE && !warp_wait(c_full, ph, wlim)) break;  // V has been read
       tc_fence_after();
-      const float2 e2 = make_float2(e, e), sc2 = make_float2(a.scale, a.scale);
+      const float2 e2 = make_float2(e, e);
 #pragma unroll 1
-      for (int x = 0; x < 2 * NV; ++x) {
-        uint32_t o1[32], o2[32];
-        tmem_ld32(tO + lanes + 32 * x, o1);
-        tmem_ld32(tX + lanes + 32 * x, o2);
-        tmem_wait_ld();
-        if (x == 2 * NV - 1) {
-          tc_fence_before();
+      for (int x0 = 0; x0 < 4 * NV; x0 += 4) {  // 32 columns
+        uint4 z[4];
+        if (gates) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if constexpr (Lay::GATE) {
+              z[x] = *reinterpret_cast<const uint4 *>(smem + Lay::Z + row + (((p8 + x0 + x) ^ swz) << 4));
+            } else {
+              z[x] = make_uint4(0u, 0u, 0u, 0u);
+              if (lane < rows && 8 * (x0 + x) < pn - first) z[x] = __ldg(reinterpret_cast<const uint4 *>(zrow + 16 * (x0 + x)));
+            }
+          }
+        }
+        if (x0 + 4 == 4 * NV) {  // the gate's tile has been read: the next one can come
           __syncwarp();
-          if (lane == 0) mbar_arrive(o_empty);
+          if (lane == 0) mbar_arrive(z_empty);
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {  // 8 columns: one 16-byte piece of v, the gate and o
-          const int piece = 4 * (x & 1) + m, col = 32 * x + 8 * m;
-          const uint32_t off = (x >> 1) * kAtom + r * 128 + ((piece ^ (r & 7)) << 4);
-          float2 y[4];
+        for (int x = 0; x < 4; ++x) {  // 8 columns: one piece of v, the gate and o
+          uint32_t o1[8], o2[8];
+          tmem_ld8(tO + lanes + 8 * (x0 + x), o1);
+          tmem_ld8(tX + lanes + 8 * (x0 + x), o2);
+          uint4 v = {};
+          if (skips) v = *reinterpret_cast<const uint4 *>(vs + (((p8 + x0 + x) ^ swz) << 4));
+          tmem_wait_ld();
+          uint32_t out[4];
+          const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, zw[4] = {z[x].x, z[x].y, z[x].z, z[x].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int q = 8 * m + 2 * i;
-            y[i] = fmul2(sc2, ffma2(e2, make_float2(__uint_as_float(o2[q]), __uint_as_float(o2[q + 1])),
-                                    make_float2(__uint_as_float(o1[q]), __uint_as_float(o1[q + 1]))));
+          for (int i = 0; i < 4; ++i) {  // columns 2 i, 2 i + 1
+            float2 y = ffma2(e2, make_float2(__uint_as_float(o2[2 * i]), __uint_as_float(o2[2 * i + 1])),
+                             make_float2(__uint_as_float(o1[2 * i]), __uint_as_float(o1[2 * i + 1])));
+            if (skips)
+              y = ffma2(*reinterpret_cast<const float2 *>(&skip[8 * (x0 + x) + 2 * i]), make_float2(bf16_lo(vw[i]), bf16_hi(vw[i])), y);
+            if (gates) y = fmul2(y, make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
+            out[i] = pack_bf16x2(y.x, y.y);
           }
-          if (a.skip) {
-            const uint4 vv = *reinterpret_cast<const uint4 *>(vs + off);
-            const float4 k0 = *reinterpret_cast<const float4 *>(&s_skip[col]);
-            const float4 k1 = *reinterpret_cast<const float4 *>(&s_skip[col + 4]);
-            y[0] = ffma2(make_float2(k0.x, k0.y), make_float2(bf16_lo(vv.x), bf16_hi(vv.x)), y[0]);
-            y[1] = ffma2(make_float2(k0.z, k0.w), make_float2(bf16_lo(vv.y), bf16_hi(vv.y)), y[1]);
-            y[2] = ffma2(make_float2(k1.x, k1.y), make_float2(bf16_lo(vv.z), bf16_hi(vv.z)), y[2]);
-            y[3] = ffma2(make_float2(k1.z, k1.w), make_float2(bf16_lo(vv.w), bf16_hi(vv.w)), y[3]);
+          *reinterpret_cast<uint4 *>(stage + (put ^ (16 * (x & 1)))) = make_uint4(out[0], out[1], out[2], out[3]);
+          if (!(x & 1)) continue;
+          __syncwarp();
+          const uint4 a0 = *reinterpret_cast<const uint4 *>(stage + get), a1 = *reinterpret_cast<const uint4 *>(stage + get + 512);
+          if (8 * (x0 + x - 1) < cols) {
+            char *dst = orow + 16 * (x0 + x - 1);
+            if (row0 < rows) st_global_v4(dst, a0.x, a0.y, a0.z, a0.w);
+            if (row0 + 16 < rows) st_global_v4(dst + 32 * a.o_row, a1.x, a1.y, a1.z, a1.w);
           }
-          if (a.gate) {
-            uint4 zz = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (Lay::TILE) zz = *reinterpret_cast<const uint4 *>(os + off);
-            else if (live && col < pn) zz = __ldg(reinterpret_cast<const uint4 *>(zp + t * a.gate_row + col));
-            y[0] = fmul2(y[0], make_float2(bf16_lo(zz.x), bf16_hi(zz.x)));
-            y[1] = fmul2(y[1], make_float2(bf16_lo(zz.y), bf16_hi(zz.y)));
-            y[2] = fmul2(y[2], make_float2(bf16_lo(zz.z), bf16_hi(zz.z)));
-            y[3] = fmul2(y[3], make_float2(bf16_lo(zz.w), bf16_hi(zz.w)));
-          }
-          const uint4 out = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
-                                       pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
-          if (!by_row) *reinterpret_cast<uint4 *>(os + off) = out;
-          else if (live && col < pn) st_global_v4(op + t * a.o_row + col, out.x, out.y, out.z, out.w);
+          __syncwarp();
         }
       }
-      fence_proxy_async();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_staged);
-      if (w == 0 && lane == 0 && one_wait(o_staged, ph, wlim)) {  // every row staged, V read
-        if (Lay::TILE) mbar_arrive(&empty[st]);
-        if (!by_row) {
-          for (int x = 0; x < NV; ++x)
-            if (64 * x < pn) tma_store_4d(&tmO, os + x * kAtom, p0 + 64 * x, h, c * C, b);
-          bulk_commit();
-          bulk_wait_read();
-        }
-        mbar_arrive(Lay::TILE ? z_empty : &empty[st]);
+      if (lane == 0) {
+        mbar_arrive(o_empty);
+        mbar_arrive(&empty[st]);  // V has been read
       }
+      if (gates) zrow += 2 * C * a.gate_row;
+      orow += 2 * C * a.o_row;
     }
-    if (w == 0 && lane == 0) bulk_wait_all();
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegState));
-    // ---------------- state: row r of the chunk's keys, row r of the state block ----------------
-    const int w = warp - 8, r = 32 * w + lane;
-    const uint32_t lanes = uint32_t(32 * w) << 16;
-    const long long dense = (long long)a.dv * a.dk;
-    const bool mine = r < pn;
-    float S[64 * NK];
-    {
-      const float *src = a.state_in + (a.state_in ? b * a.state_in_batch + h * dense + (long long)(p0 + r) * a.dk : 0);
-#pragma unroll
-      for (int n = 0; n < 64 * NK; n += 4) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (a.state_in && mine && n < a.dk) x = *reinterpret_cast<const float4 *>(src + n);
-        S[n] = x.x, S[n + 1] = x.y, S[n + 2] = x.z, S[n + 3] = x.w;
-      }
-    }
-    // the state as the operand of Q S^T: high and low bf16 parts
-    auto write_state = [&] {
-      if (r < 64 * NV) {
-        uint8_t *sb = smem + Lay::SB + r * 128;
-#pragma unroll
-        for (int n = 0; n < 64 * NK; n += 8) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 x = make_float2(S[n + 2 * i], S[n + 2 * i + 1]);
-            hi[i] = high_pair(x);
-            const float2 y = fsub2(x, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
-            lo[i] = pack_bf16x2(y.x, y.y);
-          }
-          const uint32_t off = (n >> 6) * (NV * kAtom / 2) + ((((n & 63) >> 3) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4 *>(sb + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(sb + Lay::SB_PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_proxy_async();
-      mbar_arrive(sb_full);
-    };
-    bool ok = !failed;
-    if (chunks > 0) write_state();
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::KEYS));
+    // ---------------- weighted keys: one row of the chunk per thread ----------------
+    const int r = 32 * (warp - 8) + lane;
     for (int c = 0; c < chunks; ++c) {
       const int st = c % ST;
       const uint32_t ph = uint32_t(c) & 1u;
       const int rem = len - c * C;
-      const Decays &d = dec[c & 1];
-      // weighted keys, split over three buffers whose operands have been read: the high parts
-      // over the keys, the middle parts beside them, the low parts over the queries (the
-      // scores and Q S^T are behind)
-      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim) ||
-          !warp_wait(&full[st], uint32_t(c / ST) & 1u, wlim) || !warp_wait(qs_done, ph, wlim)) {
-        ok = false;
+      // Split over three buffers whose operands have been read: the high parts over the keys,
+      // the middle parts beside them, the low parts over the queries (the scores and Q S^T of
+      // this chunk and the state product of the last one are behind).
+      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim) || !warp_wait(&full[st], uint32_t(c / ST) & 1u, wlim) ||
+          !warp_wait(c_full, ph ^ 1u, wlim) || (outputs && !warp_wait(qs_done, ph, wlim)))
         break;
-      }
-      const float wj = d.w[r], decay = d.e[C - 1];
+      const float wj = dec[c & 1].w[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
       uint8_t *krow = smem + st * Lay::STAGE + Lay::K + r * 128, *mrow = smem + Lay::MID + r * 128;
       uint8_t *qrow = smem + st * Lay::STAGE + Lay::Q + r * 128;
-#pragma unroll 2
+      const float2 w2 = make_float2(wj, wj);
+#pragma unroll 1
       for (int x = 0; x < 8 * NK; ++x) {
         const uint32_t off = (x >> 3) * kAtom + (((x & 7) ^ (r & 7)) << 4);
         uint4 kk = *reinterpret_cast<const uint4 *>(krow + off);
@@ -547,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 y = fmul2(make_float2(wj, wj), make_float2(bf16_lo(in[i]), bf16_hi(in[i])));
+          float2 y = fmul2(w2, make_float2(bf16_lo(in[i]), bf16_hi(in[i])));
           hi[i] = high_pair(y);
           y = fsub2(y, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
           mid[i] = high_pair(y);
@@ -566,35 +560,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async();
       mbar_arrive(k_full);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<NK>::STATE));
+    // ---------------- state: one row of the state block per thread ----------------
+    const int w = warp - 20, r = 32 * w + lane;
+    const uint32_t lanes = uint32_t(32 * w) << 16;
+    const long long dense = (long long)a.dv * a.dk;
+    const bool mine = r < pn;
+    float2 S[32 * NK];
+#pragma unroll
+    for (int n = 0; n < 32 * NK; ++n) S[n] = make_float2(0.f, 0.f);
+    const long long at = (long long)(p0 + r) * a.dk;  // this row in a head's state
+    // S = keep * S + the row at src
+    auto add_row = [&](const float *src, float keep) {
+#pragma unroll
+      for (int n = 0; n < 64 * NK; n += 4)
+        if (mine && n < a.dk) {
+          const float4 x = *reinterpret_cast<const float4 *>(src + at + n);
+          S[n / 2] = ffma2(make_float2(keep, keep), S[n / 2], make_float2(x.x, x.y));
+          S[n / 2 + 1] = ffma2(make_float2(keep, keep), S[n / 2 + 1], make_float2(x.z, x.w));
+        }
+    };
+    // The state the segment starts from: the sequence's first one, or the earlier segments'
+    // own states, each decayed by those after it.
+    const long long heads = (long long)a.batch * a.n_heads;
+    const float *from = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
+    if (outputs && prm.seg.n > 1) from = a.state_in ? prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense : nullptr;
+    const int first = outputs ? 0 : seg;  // a segment's own state starts from zero
+    for (int j = first; j <= seg; ++j) {
+      const float *src = j > first ? prm.seg.state + ((j - 1) * heads + bh) * dense : seg == 0 ? from : nullptr;
+      if (src) add_row(src, j > first ? exp2f((float)prm.seg.decay[(j - 1) * heads + bh]) : 0.f);
+    }
+    auto store_state = [&](float *dst) {
+#pragma unroll
+      for (int n = 0; n < 64 * NK; n += 4)
+        if (mine && n < a.dk)
+          *reinterpret_cast<float4 *>(dst + at + n) = make_float4(S[n / 2].x, S[n / 2].y, S[n / 2 + 1].x, S[n / 2 + 1].y);
+    };
+    if (!outputs && seg == 0 && a.state_in)  // a copy for the outputs' pass, which may write in place
+      store_state(prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense);
+    bool ok = !failed;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = uint32_t(c) & 1u;
+      // the state as the operand of Q S^T: high and low bf16 parts.  The buffer's last reader,
+      // the chunk before's Q S^T, is behind its P V or its state product.
+      if (outputs && !warp_wait(qs_done, ph ^ 1u, wlim)) { ok = false; break; }
+      if (outputs && r < 64 * NV) {
+        uint8_t *sb = smem + Lay::SB + r * 128;
+#pragma unroll
+        for (int n = 0; n < 64 * NK; n += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = S[n / 2 + i];
+            hi[i] = high_pair(x);
+            const float2 y = fsub2(x, make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])));
+            lo[i] = pack_bf16x2(y.x, y.y);
+          }
+          const uint32_t off = (n >> 6) * (NV * kAtom / 2) + ((((n & 63) >> 3) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4 *>(sb + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(sb + Lay::SB_PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(sb_full);
+      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) { ok = false; break; }
+      const float decay = dec[c & 1].end;
       __syncwarp();
       if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
-      // the chunk's contribution
       if (!warp_wait(c_full, ph, wlim)) { ok = false; break; }
       tc_fence_after();
+      const float2 d2 = make_float2(decay, decay);
 #pragma unroll
-      for (int n = 0; n < 64 * NK; n += 32) {
-        if (n < 16 * ksteps) {
-          uint32_t x[32], y[32];
-          tmem_ld32(tC + lanes + n, x);
-          if constexpr (NK == 1) tmem_ld32(tC + lanes + 64 + n, y);
+      for (int n = 0; n < 64 * NK; n += 16) {
+        if (n < a.dk) {  // columns from dk on stay zero
+          uint32_t x[16], y[16];
+          tmem_ld16(tC + lanes + n, x);
+          if constexpr (NK == 1) tmem_ld16(tC + lanes + 64 + n, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n + i < 16 * ksteps) {
-              const float add = NK == 1 ? __uint_as_float(x[i]) + __uint_as_float(y[i]) : __uint_as_float(x[i]);
-              S[n + i] = fmaf(decay, S[n + i], add);
-            }
+          for (int i = 0; i < 8; ++i) {
+            float2 add = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            if constexpr (NK == 1) add = fadd2(add, make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
+            S[n / 2 + i] = ffma2(d2, S[n / 2 + i], add);
+          }
         }
       }
       tc_fence_before();
-      if (c + 1 < chunks) write_state();  // Q S^T of this chunk is behind (k_full)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c_empty);
     }
-    if (ok && a.state_out && mine) {
-      float *dst = a.state_out + ((long long)b * a.n_heads + h) * dense + (long long)(p0 + r) * a.dk;
-#pragma unroll
-      for (int n = 0; n < 64 * NK; n += 4)
-        if (n < a.dk) *reinterpret_cast<float4 *>(dst + n) = make_float4(S[n], S[n + 1], S[n + 2], S[n + 3]);
-    }
+    float *dst = !outputs ? prm.seg.state + (long long)bhs * dense
+                 : a.state_out && seg == prm.seg.n - 1 ? a.state_out + (long long)bh * dense : nullptr;
+    if (ok && dst) store_state(dst);
   }
 
   tc_fence_before();
@@ -604,6 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
+
+// Blocks of the state's rows (columns of v and o): a CTA takes 64 or 128 of them.
+int dv_blocks(const hymba_linear_attention &a) { return a.dv > 64 ? (a.dv + 127) / 128 : 1; }
 
 // [batch, rows, heads, dim] bf16 as a 4-D map, boxes of 128 rows of 64 columns of one head.
 bool head_map(CUtensorMap *map, const void *p, long long batch, long long rows, long long heads, int dim,
@@ -618,7 +680,7 @@ bool head_map(CUtensorMap *map, const void *p, long long batch, long long rows, 
 }
 
 template <int NK, int NV>
-hymba_status chunk_launch(const hymba_linear_attention &a, cudaStream_t s) {
+hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, cudaStream_t s) {
   using Lay = Layout<NK, NV>;
   static_assert(Lay::TOTAL <= 232448, "shared memory of one CTA");
   static DeviceOnce attr_set;
@@ -632,28 +694,30 @@ hymba_status chunk_launch(const hymba_linear_attention &a, cudaStream_t s) {
     }
     attr_set.mark(dev);
   }
-  CUtensorMap tq, tk, tv, tz, to;
+  CUtensorMap tq, tk, tv, tz;
   if (!head_map(&tq, a.q, a.batch, a.n_rows, a.n_qk_heads, a.dk, a.q_batch, a.q_row, a.q_head) ||
       !head_map(&tk, a.k, a.batch, a.n_rows, a.n_qk_heads, a.dk, a.k_batch, a.k_row, a.k_head) ||
-      !head_map(&tv, a.v, a.batch, a.n_rows, a.n_heads, a.dv, a.v_batch, a.v_row, a.v_head) ||
-      !head_map(&to, a.o, a.batch, a.n_rows, a.n_heads, a.dv, a.o_batch, a.o_row, a.o_head))
+      !head_map(&tv, a.v, a.batch, a.n_rows, a.n_heads, a.dv, a.v_batch, a.v_row, a.v_head))
     return HYMBA_ERR_CUDA;
   tz = tv;
   if (a.gate && !head_map(&tz, a.gate, a.batch, a.n_rows, a.n_heads, a.dv, a.gate_batch, a.gate_row, a.gate_head))
     return HYMBA_ERR_CUDA;
   Params p{};
   p.a = a;
-  p.blocks = (a.dv + 64 * NV - 1) / (64 * NV);
+  p.seg = seg;
+  p.blocks = dv_blocks(a);
   const long long cycles = wait_limit_cycles();
   p.wlim = cycles > 0x7fffffffLL ? 0x7fffffffu : (unsigned)cycles;
-  const long long grid = (long long)a.batch * a.n_heads * p.blocks;
-  if (grid > 0x7fffffffLL) {
+  const long long ctas = (long long)a.batch * a.n_heads * p.blocks;
+  if (ctas * seg.n > 0x7fffffffLL) {
     set_error("too many sequences and heads");
     return HYMBA_ERR_UNSUPPORTED;
   }
-  launch_kernel(linear_chunk_kernel<NK, NV>, dim3((unsigned)grid), dim3(kThreads), (size_t)Lay::TOTAL, s, tq, tk, tv, tz, to,
-                p);
-  note_launch(1);
+  for (p.seg.pass = seg.n > 1 ? 0 : 1; p.seg.pass < 2; ++p.seg.pass) {
+    const long long grid = ctas * (p.seg.pass ? seg.n : seg.n - 1);
+    launch_kernel(linear_chunk_kernel<NK, NV>, dim3((unsigned)grid), dim3(kThreads), (size_t)Lay::TOTAL, s, tq, tk, tv, tz, p);
+    note_launch(1);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("linear attention launch failed: %s", cudaGetErrorString(e));
@@ -664,10 +728,28 @@ hymba_status chunk_launch(const hymba_linear_attention &a, cudaStream_t s) {
 
 }  // namespace
 
-hymba_status linear_attention_tc(const hymba_linear_attention &a, cudaStream_t s) {
+// One CTA takes a whole SM, a head's chunks one after another.  When the heads leave SMs idle
+// the rows are split into segments, as many as fit beside each other: the segments' own
+// states first (about 0.6 of a chunk's time each), then their outputs.  That takes 1.6 / n of
+// the time in n segments, and a second launch about as long as four chunks: 25 heads of 8320
+// rows 450 us whole and 163 us in five segments, 28 heads of 517 rows 18 us whole and 28 us
+// in two.
+LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a) {
+  LinearSegments g{};
+  const long long ctas = (long long)a.batch * a.n_heads * dv_blocks(a);
+  const int chunks = (a.n_rows + C - 1) / C;
+  const long long most = std::max<long long>(1, std::min<long long>(148 / std::max<long long>(1, ctas), chunks / 2));
+  const int per = (chunks + (int)most - 1) / (int)most, n = (chunks + per - 1) / per;
+  const bool split = 5 * chunks * (long long)n - 8 * chunks >= 20 * (long long)n;  // chunks (1 - 1.6 / n) >= 4
+  g.n = split ? n : 1;
+  g.rows = (split ? per : chunks) * C;
+  return g;
+}
+
+hymba_status linear_attention_tc(const hymba_linear_attention &a, const LinearSegments &seg, cudaStream_t s) {
   const bool wide_k = a.dk > 64, wide_v = a.dv > 64;
-  if (wide_k) return wide_v ? chunk_launch<2, 2>(a, s) : chunk_launch<2, 1>(a, s);
-  return wide_v ? chunk_launch<1, 2>(a, s) : chunk_launch<1, 1>(a, s);
+  if (wide_k) return wide_v ? chunk_launch<2, 2>(a, seg, s) : chunk_launch<2, 1>(a, seg, s);
+  return wide_v ? chunk_launch<1, 2>(a, seg, s) : chunk_launch<1, 1>(a, seg, s);
 }
 
 unsigned take_error_linear() {

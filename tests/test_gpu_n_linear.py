@@ -81,6 +81,12 @@ CASES = [
     ("bf16", 1, 200, 2, 1, 104, 136, "strong", True, True, None),
     ("bf16", 5, 260, 2, 1, 64, 128, "token", True, True, [0, 1, 128, 200, 999]),
     ("bf16", 4, 37, 2, 2, 32, 32, "head", False, False, [37, -3, 36, 2]),
+    # rows split over the SMs: segments' states first, then their outputs
+    ("bf16", 2, 1000, 2, 1, 64, 128, "token", True, True, None),
+    ("bf16", 3, 900, 2, 2, 128, 72, "head", True, True, [0, 130, 900]),
+    ("bf16", 1, 1290, 1, 1, 16, 200, "strong", False, False, None),
+    # few rows: one after another
+    ("bf16", 2, 9, 3, 1, 72, 40, "token", True, True, [9, 4]),
     ("f32", 2, 1, 4, 1, 64, 128, "token", True, True, None),
     ("f32", 2, 33, 4, 2, 64, 128, "token", True, True, None),
     ("f32", 1, 200, 3, 1, 128, 72, "head", True, True, None),
@@ -147,11 +153,11 @@ def test_no_decay_and_null_options():
     assert torch.equal(o, o2)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_strided_views_and_states_in_place(dtype):
+@pytest.mark.parametrize("dtype,L", [("bf16", 135), ("f32", 135), ("bf16", 1100)])
+def test_strided_views_and_states_in_place(dtype, L):
     """q, k, v, gate as slices of one fused row, heads outermost in o, one state for every sequence,
-    then the state continued in place."""
-    B, L, H, K, dk, dv = 2, 135, 4, 2, 32, 64
+    then the state continued in place (with 1100 rows by segments, whose first one reads it)."""
+    B, H, K, dk, dv = 2, 4, 2, 32, 64
     x = inputs(dtype, B, L, H, K, dk, dv)
     x["state_in"] = x["state_in"][:1].expand(B, -1, -1, -1)
     width = 2 * K * dk + 2 * H * dv + 32
