@@ -24,65 +24,52 @@ struct HeadsParams {
   double turns[kMaxPairs];  // f_i / (2 pi): turns per position
 };
 
-// Eight elements of a head as one (bf16) or two (fp32) 16-byte vectors.
+// Four elements of a head: 8 bytes of bf16, 16 of fp32.
 template <typename T>
-struct Vec8;
+struct Vec4;
 template <>
-struct Vec8<__nv_bfloat16> {
-  uint4 r;
-  __device__ __forceinline__ void load(const void *p) { r = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(w[i]);
-      x[2 * i + 1] = bf16_hi(w[i]);
-    }
+struct Vec4<__nv_bfloat16> {
+  using R = uint2;
+  static __device__ __forceinline__ void get(const R &r, float *x) {
+    x[0] = bf16_lo(r.x), x[1] = bf16_hi(r.x), x[2] = bf16_lo(r.y), x[3] = bf16_hi(r.y);
   }
-  static __device__ __forceinline__ void store(void *p, const float (&x)[8]) {
-    st_global_v4(p, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                 pack_bf16x2(x[6], x[7]));
+  static __device__ __forceinline__ R put(const float *x) {
+    return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
   }
 };
 template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void *p) {
-    a = reinterpret_cast<const float4 *>(p)[0];
-    b = reinterpret_cast<const float4 *>(p)[1];
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  static __device__ __forceinline__ void store(void *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
+struct Vec4<float> {
+  using R = float4;
+  static __device__ __forceinline__ void get(const R &r, float *x) { x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w; }
+  static __device__ __forceinline__ R put(const float *x) { return make_float4(x[0], x[1], x[2], x[3]); }
 };
 
-// How an element finds its pair's other element.
+// Which eight elements of a head a lane holds, and where an element's pair is.
 enum Partner {
-  kNone,      // no rotation
-  kInLane,    // pairs (2i, 2i+1): in the same lane
-  kByShuffle, // halves dim/2 = 8 n apart: the same element of the lane n away
-  kByShared   // other halves: through shared memory
+  kNone,    // no rotation: elements 8 l ..
+  kPairs,   // pairs (2i, 2i+1): elements 8 l .., four pairs
+  kHalves,  // halves of the whole head: elements 4 l .. and d/2 + 4 l .., four pairs
+  kShared   // halves of a part of the head: elements 8 l .., the pairs through shared memory
 };
 
 // A warp takes one unit: a row of a sequence and a share of its heads.  Its lanes first
 // compute the row's angles, one pair each (fp64 turns p * f / 2 pi, of which only the
-// fraction goes to the fp32 sincospi), and keep the factors of their own eight elements in
-// registers for all heads of the unit.  32 / lanes heads are in flight per load, four loads
-// ahead of the arithmetic.
+// fraction goes to the fp32 sincospi), and keep the factors of their own pairs in registers
+// for all heads of the unit.  32 / lanes heads are in flight per load, kAhead loads ahead of
+// the arithmetic.
+//
+// Bound by instructions more than by HBM: per element a share of the conversions, of the
+// norm's sum over the head's lanes and of the rotation.  With a head's halves in lanes of
+// their own the rotation took eight shuffles per eight elements (109 us at 8 x 4224 rows of
+// 30 heads); a lane that holds both elements of its pairs needs none.
 template <typename T, int PARTNER>
 __global__ void __launch_bounds__(32 * kHeadWarps)
     qk_norm_rope_kernel(const __grid_constant__ HeadsParams p) {
   pdl_wait();
   pdl_trigger();
+  using V = Vec4<T>;
   __shared__ float2 s_trig[PARTNER == kNone ? 1 : kHeadWarps * kMaxPairs];
-  __shared__ float s_stage[PARTNER == kByShared ? kHeadWarps * 256 : 1];
+  __shared__ float s_stage[PARTNER == kShared ? kHeadWarps * 256 : 1];
   const hymba_qk_norm_rope_args &a = p.a;
   const int warp = warp_id(), lane = lane_id();
   const long long unit = (long long)blockIdx.x * kHeadWarps + warp;
@@ -92,11 +79,14 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   const int r = int(row_id % a.n_rows);
   const long long b = row_id / a.n_rows;
   const int lanes = p.lanes, li = lane & (lanes - 1), slot = lane / lanes, per = 32 / lanes;
-  const int d = a.head_dim, e0 = 8 * li;
-  const bool live = e0 < d;
-  const int rot = a.rope.dim, half = rot >> 1;
+  const int d = a.head_dim, rot = a.rope.dim, half = rot >> 1;
+  const bool live = 8 * li < d;
+  // the lane's elements: four from e0, four from e1
+  const int e0 = PARTNER == kHalves ? 4 * li : 8 * li, e1 = PARTNER == kHalves ? half + 4 * li : e0 + 4;
 
-  float cs[PARTNER == kNone ? 1 : 8], sn[PARTNER == kNone ? 1 : 8];
+  // kPairs, kHalves: cos and sin of the lane's four pairs; kShared: of its eight elements'
+  constexpr int NF = PARTNER == kNone ? 1 : PARTNER == kShared ? 8 : 4;
+  float cs[NF], sn[NF];
   if constexpr (PARTNER != kNone) {
     const double pos = double(a.pos0 + (a.positions ? a.positions[row_id] : (long long)r));
     float2 *trig = s_trig + warp * kMaxPairs;
@@ -108,56 +98,53 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
       trig[i] = make_float2(c * a.rope.attn_factor, s * a.rope.attn_factor);
     }
     __syncwarp();
-    // y_e = x_e c_e + x_partner s_e, with c = 1, s = 0 behind the rotated part
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = e0 + j;
-      cs[j] = 1.f;
-      sn[j] = 0.f;
-      if (e < rot) {
-        const bool second = PARTNER == kInLane ? (e & 1) : e >= half;
-        const float2 t = trig[PARTNER == kInLane ? e >> 1 : second ? e - half : e];
-        cs[j] = t.x;
-        sn[j] = second ? t.y : -t.y;
-      }
+    for (int j = 0; j < NF; ++j) {
+      const int i = PARTNER == kPairs ? 4 * li + j : PARTNER == kHalves ? e0 + j : e0 + j < half ? e0 + j : e0 + j - half;
+      const float2 t = i < half ? trig[i] : make_float2(1.f, 0.f);  // behind the rotated part
+      cs[j] = t.x;
+      sn[j] = PARTNER == kShared && e0 + j < half ? -t.y : t.y;
     }
   }
 
-  const int heads = a.q.n_heads + a.k.n_heads;
+  const int nq = a.q.n_heads, heads = nq + a.k.n_heads;
   const int groups = (heads + per - 1) / per;
   const float inv_d = 1.0f / float(d);
+  const T *qi = reinterpret_cast<const T *>(a.q.in) + b * a.q.in_batch + r * a.q.in_row;
+  const T *ki = reinterpret_cast<const T *>(a.k.in) + b * a.k.in_batch + r * a.k.in_row;
+  T *qo = reinterpret_cast<T *>(a.q.out) + b * a.q.out_batch + r * a.q.out_row;
+  T *ko = reinterpret_cast<T *>(a.k.out) + b * a.k.out_batch + r * a.k.out_row;
   for (int g0 = part * p.chunk; g0 < groups; g0 += p.parts * p.chunk) {
-    Vec8<T> raw[kAhead];
+    typename V::R ra[kAhead], rb[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int hh = (g0 + u) * per + slot;
-      raw[u].zero();
+      ra[u] = rb[u] = typename V::R{};
       if (live && u < p.chunk && hh < heads) {
-        const bool is_q = hh < a.q.n_heads;
-        const long long at = b * (is_q ? a.q.in_batch : a.k.in_batch) + r * (is_q ? a.q.in_row : a.k.in_row) +
-                             (is_q ? hh * a.q.in_head : (hh - a.q.n_heads) * a.k.in_head) + e0;
-        raw[u].load(reinterpret_cast<const T *>(is_q ? a.q.in : a.k.in) + at);
+        const T *src = hh < nq ? qi + hh * a.q.in_head : ki + (hh - nq) * a.k.in_head;
+        ra[u] = *reinterpret_cast<const typename V::R *>(src + e0);
+        rb[u] = *reinterpret_cast<const typename V::R *>(src + e1);
       }
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (u >= p.chunk || g0 + u >= groups) break;  // the same for the whole warp
       const int hh = (g0 + u) * per + slot;
-      const bool is_q = hh < a.q.n_heads;
       float x[8];
-      raw[u].get(x);
+      V::get(ra[u], x);
+      V::get(rb[u], x + 4);
       if (a.norm) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
         for (int m = lanes >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float inv = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
+        const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= inv;
-        const float *weight = is_q ? a.q.weight : a.k.weight;
-        if (weight && live && hh < heads) {
+        const float *weight = hh < nq ? a.q.weight : a.k.weight;
+        if (weight && live) {
           const float4 w0 = __ldg(reinterpret_cast<const float4 *>(weight + e0));
-          const float4 w1 = __ldg(reinterpret_cast<const float4 *>(weight + e0) + 1);
+          const float4 w1 = __ldg(reinterpret_cast<const float4 *>(weight + e1));
           const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] *= w[j];
@@ -167,16 +154,16 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
       if constexpr (PARTNER == kNone) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = x[j];
-      } else if constexpr (PARTNER == kInLane) {
+      } else if constexpr (PARTNER == kPairs || PARTNER == kHalves) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = e0 + j < rot ? fmaf(x[j], cs[j], x[j ^ 1] * sn[j]) : x[j];
-      } else if constexpr (PARTNER == kByShuffle) {
-        const int away = half >> 3;
-        const int from = e0 < half ? lane + away : e0 < rot ? lane - away : lane;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float o = __shfl_sync(0xffffffffu, x[j], from);
-          y[j] = e0 + j < rot ? fmaf(x[j], cs[j], o * sn[j]) : x[j];
+        for (int j = 0; j < 4; ++j) {
+          const int f = PARTNER == kPairs ? 2 * j : j, s = PARTNER == kPairs ? 2 * j + 1 : j + 4;
+          y[f] = fmaf(x[f], cs[j], -x[s] * sn[j]);
+          y[s] = fmaf(x[s], cs[j], x[f] * sn[j]);
+          if (PARTNER == kPairs && e0 + 2 * j >= rot) {  // not rotated: as it is, whatever its pair holds
+            y[f] = x[f];
+            y[s] = x[s];
+          }
         }
       } else {
         // each lane's eight elements at 8 lane: the warp's heads side by side
@@ -193,9 +180,9 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
         }
       }
       if (live && hh < heads) {
-        const long long at = b * (is_q ? a.q.out_batch : a.k.out_batch) + r * (is_q ? a.q.out_row : a.k.out_row) +
-                             (is_q ? hh * a.q.out_head : (hh - a.q.n_heads) * a.k.out_head) + e0;
-        Vec8<T>::store(reinterpret_cast<T *>(is_q ? a.q.out : a.k.out) + at, y);
+        T *dst = hh < nq ? qo + hh * a.q.out_head : ko + (hh - nq) * a.k.out_head;
+        *reinterpret_cast<typename V::R *>(dst + e0) = V::put(y);
+        *reinterpret_cast<typename V::R *>(dst + e1) = V::put(y + 4);
       }
     }
   }
@@ -205,9 +192,9 @@ template <typename T>
 void heads_launch(const HeadsParams &p, int partner, unsigned grid, cudaStream_t s) {
   const dim3 g(grid), blk(32 * kHeadWarps);
   if (partner == kNone) launch_kernel(qk_norm_rope_kernel<T, kNone>, g, blk, 0, s, p);
-  else if (partner == kInLane) launch_kernel(qk_norm_rope_kernel<T, kInLane>, g, blk, 0, s, p);
-  else if (partner == kByShuffle) launch_kernel(qk_norm_rope_kernel<T, kByShuffle>, g, blk, 0, s, p);
-  else launch_kernel(qk_norm_rope_kernel<T, kByShared>, g, blk, 0, s, p);
+  else if (partner == kPairs) launch_kernel(qk_norm_rope_kernel<T, kPairs>, g, blk, 0, s, p);
+  else if (partner == kHalves) launch_kernel(qk_norm_rope_kernel<T, kHalves>, g, blk, 0, s, p);
+  else launch_kernel(qk_norm_rope_kernel<T, kShared>, g, blk, 0, s, p);
 }
 
 }  // namespace
@@ -232,8 +219,8 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
   }
   for (int i = half; i < kMaxPairs; ++i) p.turns[i] = 0.0;
   const int partner = half == 0 ? kNone
-                      : a.rope.layout == HYMBA_ROPE_PAIRS ? kInLane
-                      : half % 8 == 0 ? kByShuffle : kByShared;
+                      : a.rope.layout == HYMBA_ROPE_PAIRS ? kPairs
+                      : a.rope.dim == a.head_dim ? kHalves : kShared;
   // One warp per row amortises the row's angles over all of its heads; with too few rows to
   // give every SM 16 warps, a row's heads are split over several warps, down to one load of
   // 32 / lanes heads each.

@@ -27,18 +27,23 @@ __device__ __forceinline__ float4 load4(const T *p) {
 }
 
 // Bound by the state's bytes, read and written once.  A CTA takes `rows` of the dv state
-// rows of one (sequence, head); `lanes` lanes (a power of two) hold one row, four columns
-// each, so a warp's loads and stores are whole contiguous rows.
-template <typename T>
-__global__ void __launch_bounds__(32 * kStepWarps)
-    linear_step_kernel(const __grid_constant__ hymba_linear_attention a, int lanes, int rows) {
+// rows of one (sequence, head); LANES lanes hold one row, four columns each, so a warp's loads
+// and stores are whole contiguous rows.  A lane's eight rows are requested together.  Their
+// dot products with q are summed over the lanes by halves: each exchange hands half of the
+// rows' sums to the other half of the lanes, so eight sums over LANES >= 8 lanes take 7 +
+// log2(LANES / 8) shuffles and each lands in a lane of its own, which finishes that row.
+template <typename T, int LANES>
+__global__ void __launch_bounds__(32 * kStepWarps, 4)
+    linear_step_kernel(const __grid_constant__ hymba_linear_attention a, int rows) {
   pdl_wait();
   pdl_trigger();
+  constexpr int PER = 32 / LANES;           // state rows per warp and load
+  constexpr int STRIDE = kStepWarps * PER;  // rows of the CTA per load
+  constexpr int KEPT = LANES >= kStepAhead ? 1 : kStepAhead / LANES;  // rows' sums a lane ends up with
   const int h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (a.n_heads / a.n_qk_heads);
-  const int lane = lane_id(), li = lane & (lanes - 1), c0 = 4 * li;
+  const int lane = lane_id(), li = lane % LANES, c0 = 4 * li;
   const bool live = c0 < a.dk;
-  const int per = 32 / lanes;  // state rows per warp and load
   const int p_end = min(a.dv, (int)(blockIdx.x + 1) * rows);
   const long long dense = (long long)a.dv * a.dk;
   const float *sin = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
@@ -55,14 +60,20 @@ __global__ void __launch_bounds__(32 * kStepWarps)
     k = load4(reinterpret_cast<const T *>(a.k) + b * a.k_batch + hk * a.k_head + c0);
     q = load4(reinterpret_cast<const T *>(a.q) + b * a.q_batch + hk * a.q_head + c0);
   }
-  const int stride = kStepWarps * per;
-  for (int p0 = blockIdx.x * rows + warp_id() * per + lane / lanes; p0 - lane / lanes < p_end;
-       p0 += kStepAhead * stride) {
+  // which of its eight rows' sums a lane ends up with, from its number's high bits down; of
+  // the lanes that share one the first finishes it
+  int u0 = 0;
+#pragma unroll
+  for (int m = LANES / 2, n = kStepAhead / 2; m > 0 && n > 0; m >>= 1, n >>= 1)
+    if (li & m) u0 += n;
+  const bool finishes = LANES <= kStepAhead || li % (LANES > kStepAhead ? LANES / kStepAhead : 1) == 0;
+  for (int base = blockIdx.x * rows; base < p_end; base += kStepAhead * STRIDE) {
+    const int p0 = base + warp_id() * PER + lane / LANES;
     float4 st[kStepAhead];
-    float v[kStepAhead];
+    float v[kStepAhead], dot[kStepAhead], skip[KEPT], gate[KEPT], vr[KEPT];
 #pragma unroll
     for (int u = 0; u < kStepAhead; ++u) {
-      const int p = p0 + u * stride;
+      const int p = p0 + u * STRIDE;
       st[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       v[u] = 0.f;
       if (p < p_end) {
@@ -71,8 +82,16 @@ __global__ void __launch_bounds__(32 * kStepWarps)
       }
     }
 #pragma unroll
+    for (int i = 0; i < KEPT; ++i) {
+      const int p = p0 + (u0 + i) * STRIDE;
+      const bool in = finishes && p < p_end;
+      vr[i] = in ? Store<T>::to_f(vp[p]) : 0.f;
+      skip[i] = in && a.skip ? a.skip[(long long)h * a.dv + p] : 0.f;
+      gate[i] = in && a.gate ? Store<T>::to_f(zp[p]) : 1.f;
+    }
+#pragma unroll
     for (int u = 0; u < kStepAhead; ++u) {
-      const int p = p0 + u * stride;
+      const int p = p0 + u * STRIDE;
       const float x = s * v[u];
       if (!idle) {
         st[u].x = fmaf(decay, st[u].x, x * k.x);
@@ -80,17 +99,30 @@ __global__ void __launch_bounds__(32 * kStepWarps)
         st[u].z = fmaf(decay, st[u].z, x * k.z);
         st[u].w = fmaf(decay, st[u].w, x * k.w);
       }
-      float dot = fmaf(st[u].x, q.x, st[u].y * q.y) + fmaf(st[u].z, q.z, st[u].w * q.w);
-      for (int m = lanes >> 1; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-      if (p < p_end) {
-        if (live) *reinterpret_cast<float4 *>(sout + (long long)p * a.dk + c0) = st[u];
-        if (li == 0 && !idle) {
-          float y = a.scale * dot;
-          if (a.skip) y = fmaf(a.skip[(long long)h * a.dv + p], v[u], y);
-          if (a.gate) y *= Store<T>::to_f(zp[p]);
-          op[p] = Store<T>::from_f(y);
-        }
+      dot[u] = fmaf(st[u].x, q.x, st[u].y * q.y) + fmaf(st[u].z, q.z, st[u].w * q.w);
+      if (live && p < p_end) *reinterpret_cast<float4 *>(sout + (long long)p * a.dk + c0) = st[u];
+    }
+    int n = kStepAhead / 2;
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1) {
+      if (n > 0) {
+        const bool upper = li & m;
+#pragma unroll
+        for (int i = 0; i < kStepAhead / 2; ++i)
+          if (i < n) {
+            const float give = upper ? dot[i] : dot[i + n];
+            dot[i] = (upper ? dot[i + n] : dot[i]) + __shfl_xor_sync(0xffffffffu, give, m);
+          }
+        n >>= 1;
+      } else {
+        dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], m);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) {
+      const int p = p0 + (u0 + i) * STRIDE;
+      if (finishes && p < p_end && !idle)
+        op[p] = Store<T>::from_f(fmaf(skip[i], vr[i], a.scale * dot[i]) * gate[i]);
     }
   }
 }
@@ -314,8 +346,10 @@ LinearSegments scan_segments(const hymba_linear_attention &a) {
   return g;
 }
 
-// Below this many rows a bf16 sequence is taken row by row: a chunk costs its 128 rows
-// however many count.
+// Below this many rows a bf16 sequence is taken row by row: a chunk costs its 128 rows however
+// many count.  Row by row and in a chunk: 25 heads 9.6 and 10.5 us at 16 rows, 13.3 and 10.6 at
+// 24; 200 heads 13.4 and 21.3 us at 16, 21.1 and 21.1 at 32; 800 heads with dk 128 104 and 91 us
+// at 12 and 16, 129 and 91 at 16.
 constexpr int kFewRows = 16;
 bool on_tensor_cores(const hymba_linear_attention &a) { return a.dtype == HYMBA_BF16 && a.n_rows >= kFewRows; }
 LinearSegments segments_of(const hymba_linear_attention &a) {
@@ -328,7 +362,7 @@ size_t segment_state_bytes(const hymba_linear_attention &a, const LinearSegments
 }  // namespace
 
 hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s) {
-  int lanes = 1;
+  int lanes = 2;
   while (lanes * 4 < a.dk) lanes *= 2;
   // One CTA for all state rows of a (sequence, head) keeps eight loads in flight per lane;
   // with fewer (sequence, head) pairs than two CTAs for each SM the rows are split, down to
@@ -339,11 +373,16 @@ hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t
   const long long want = (2 * 148 + pairs - 1) / pairs;
   const int parts = int(want < most ? want : most);
   const int rows = (most + parts - 1) / parts * once;
-  const dim3 grid((a.dv + rows - 1) / rows, a.n_heads, a.batch);
-  if (a.dtype == HYMBA_BF16)
-    launch_kernel(linear_step_kernel<__nv_bfloat16>, grid, dim3(32 * kStepWarps), 0, s, a, lanes, rows);
-  else
-    launch_kernel(linear_step_kernel<float>, grid, dim3(32 * kStepWarps), 0, s, a, lanes, rows);
+  const dim3 grid((a.dv + rows - 1) / rows, a.n_heads, a.batch), block(32 * kStepWarps);
+  auto launch = [&](auto *bf16, auto *f32) {
+    if (a.dtype == HYMBA_BF16) launch_kernel(bf16, grid, block, 0, s, a, rows);
+    else launch_kernel(f32, grid, block, 0, s, a, rows);
+  };
+  if (lanes == 2) launch(linear_step_kernel<__nv_bfloat16, 2>, linear_step_kernel<float, 2>);
+  else if (lanes == 4) launch(linear_step_kernel<__nv_bfloat16, 4>, linear_step_kernel<float, 4>);
+  else if (lanes == 8) launch(linear_step_kernel<__nv_bfloat16, 8>, linear_step_kernel<float, 8>);
+  else if (lanes == 16) launch(linear_step_kernel<__nv_bfloat16, 16>, linear_step_kernel<float, 16>);
+  else launch(linear_step_kernel<__nv_bfloat16, 32>, linear_step_kernel<float, 32>);
   return launched("linear attention step");
 }
 
