@@ -100,6 +100,16 @@ class hymba_linear_attention(C.Structure):
                  ("state_out", C.c_void_p), ("lengths", C.c_void_p)])
 
 
+class hymba_layer_heads(C.Structure):
+    _fields_ = [("norm", C.c_int), ("eps", C.c_float), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p),
+                ("rope", hymba_rope)]
+
+
+class hymba_linear_heads(C.Structure):
+    _fields_ = [("d_state", C.c_int), ("w_x", C.c_void_p), ("b_dt", C.c_void_p), ("a_log", C.c_void_p),
+                ("d_skip", C.c_void_p)]
+
+
 class hymba_profile_entry(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("calls", C.c_int), ("kernels", C.c_int),
                 ("total_ms", C.c_double)]
@@ -149,6 +159,8 @@ _SIGS = {
     "hymba_layer_decode_step": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_void_p, C.c_void_p,
                                           C.POINTER(hymba_kv_cache), C.POINTER(hymba_ssm_cache),
                                           C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hymba_layer_set_heads": (C.c_int, [C.c_void_p, C.POINTER(hymba_layer_heads)]),
+    "hymba_layer_set_linear_heads": (C.c_int, [C.c_void_p, C.POINTER(hymba_linear_heads)]),
     "hymba_qk_norm_rope": (C.c_int, [C.POINTER(hymba_qk_norm_rope_args), C.c_void_p]),
     "hymba_linear_attention_workspace": (C.c_int, [C.POINTER(hymba_linear_attention), C.POINTER(C.c_size_t)]),
     "hymba_linear_attention_prefill": (C.c_int, [C.POINTER(hymba_linear_attention), C.c_void_p, C.c_size_t,
@@ -354,6 +366,15 @@ def hymba_layer_decode_step_static(layer: int, batch: int, pos: int, x_t, y_t,
                                                _stream(stream)), "hymba_layer_decode_step_static")
 
 
+def hymba_layer_set_heads(layer: int, heads: hymba_layer_heads | None) -> None:
+    check(lib().hymba_layer_set_heads(layer, C.byref(heads) if heads is not None else None), "hymba_layer_set_heads")
+
+
+def hymba_layer_set_linear_heads(layer: int, heads: hymba_linear_heads | None) -> None:
+    check(lib().hymba_layer_set_linear_heads(layer, C.byref(heads) if heads is not None else None),
+          "hymba_layer_set_linear_heads")
+
+
 def hymba_qk_norm_rope(args: hymba_qk_norm_rope_args, stream=None) -> None:
     check(lib().hymba_qk_norm_rope(C.byref(args), _stream(stream)), "hymba_qk_norm_rope")
 
@@ -545,3 +566,13 @@ def make_linear_attention(q, k, v, o, log_decay=None, in_scale=None, skip=None, 
     a.state_out = _dense("state_out", state_out, (B, H, dv, dk), "torch.float32")
     a.lengths = _dense("lengths", lengths, (B,), "torch.int32")
     return a
+
+
+def make_layer_heads(norm: bool = True, eps: float = 1e-6, q_weight=None, k_weight=None,
+                     rope: hymba_rope | None = None) -> hymba_layer_heads:
+    return hymba_layer_heads(int(norm), eps, _ptr(q_weight), _ptr(k_weight), rope if rope is not None else hymba_rope())
+
+
+def make_linear_heads(w: dict, d_state: int) -> hymba_linear_heads:
+    """From device tensors w_x [2 * d_state + n_heads, d_inner], b_dt and a_log [n_heads], d_skip [d_inner]."""
+    return hymba_linear_heads(d_state, *[_ptr(w[n]) for n in ("w_x", "b_dt", "a_log", "d_skip")])

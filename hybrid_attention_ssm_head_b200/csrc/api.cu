@@ -104,6 +104,10 @@ struct hymba_layer {
   const hymba_layer *producer;  // non-null for a K/V-sharing consumer
   uint64_t producer_id;
   BranchStreams br;
+  bool heads_on = false;         // hymba_layer_set_heads
+  hymba_layer_heads heads = {};
+  bool linear_on = false;        // hymba_layer_set_linear_heads
+  hymba_linear_heads linear = {};
 };
 
 static void branch_release(BranchStreams &b) {
@@ -155,6 +159,15 @@ static int qk_width(const hymba_layer_config &c) { return c.n_heads * c.head_dim
 static int k_width(const hymba_layer_config &c) { return c.n_kv_heads * c.head_dim_qk; }
 static int v_width(const hymba_layer_config &c) { return c.n_kv_heads * c.head_dim_v; }
 static int xdbl_width(const hymba_layer_config &c) { return c.dt_rank + 2 * c.d_state; }
+// Columns of the SSM branch's projection, and the states of a channel.
+static int ssm_proj_width(const hymba_layer &l) {
+  return l.linear_on ? 2 * l.linear.d_state + l.cfg.n_heads : xdbl_width(l.cfg);
+}
+static int ssm_states(const hymba_layer &l) { return l.linear_on ? l.linear.d_state : l.cfg.d_state; }
+// Row stride of that projection in the prefill: linear heads' odd widths padded for vector stores.
+static int ssm_proj_ld(const hymba_layer &l) {
+  return l.linear_on ? (ssm_proj_width(l) + 15) / 16 * 16 : xdbl_width(l.cfg);
+}
 static float score_scale(const hymba_layer_config &c) {
   return c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt((float)c.head_dim_qk);
 }
@@ -261,6 +274,122 @@ hymba_status hymba_kv_share_bind(hymba_layer *consumer, const hymba_layer *produ
 }
 
 // ---------------------------------------------------------------------------
+// operators inside the layer
+// ---------------------------------------------------------------------------
+hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *heads) {
+  g_msg[0] = 0;
+  if (!layer) FAIL(HYMBA_ERR_INVALID_ARG, "null layer");
+  if (!heads) {
+    layer->heads_on = false;
+    return HYMBA_OK;
+  }
+  const hymba_layer_config &c = layer->cfg;
+  if (c.head_dim_qk % 8) FAIL(HYMBA_ERR_UNSUPPORTED, "head_dim_qk must be a multiple of 8");
+  const hymba_status st = check_rope(heads->rope, c.head_dim_qk);
+  if (st != HYMBA_OK) return st;
+  if (heads->rope.dim > 0 && c.rope_base > 0.f) FAIL(HYMBA_ERR_INVALID_ARG, "the layer has a rotation already (rope_base)");
+  if (heads->norm && (!(heads->eps >= 0.f) || !std::isfinite(heads->eps))) FAIL(HYMBA_ERR_INVALID_ARG, "eps < 0");
+  if (!heads->norm && (heads->q_weight || heads->k_weight)) FAIL(HYMBA_ERR_INVALID_ARG, "a weight without the norm");
+  if (!aligned16(heads->q_weight) || !aligned16(heads->k_weight))
+    FAIL(HYMBA_ERR_INVALID_ARG, "weight pointer not 16-byte aligned");
+  layer->heads = *heads;
+  layer->heads_on = true;
+  return HYMBA_OK;
+}
+
+hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hymba_linear_heads *heads) {
+  g_msg[0] = 0;
+  if (!layer) FAIL(HYMBA_ERR_INVALID_ARG, "null layer");
+  if (!heads) {
+    layer->linear_on = false;
+    return HYMBA_OK;
+  }
+  const hymba_layer_config &c = layer->cfg;
+  if (heads->d_state < 8 || heads->d_state % 8 || heads->d_state > 128)
+    FAIL(HYMBA_ERR_UNSUPPORTED, "d_state %d: a multiple of 8 up to 128", heads->d_state);
+  if (c.head_dim_v % 8 || c.head_dim_v > 256) FAIL(HYMBA_ERR_UNSUPPORTED, "head_dim_v must be a multiple of 8 up to 256");
+  // the decode step keeps 128 channels of the projection in shared memory
+  if (2 * heads->d_state + c.n_heads > 360) FAIL(HYMBA_ERR_UNSUPPORTED, "2 * d_state + n_heads > 360");
+  for (const void *p : {heads->w_x, (const void *)heads->b_dt, (const void *)heads->a_log, (const void *)heads->d_skip})
+    if (!p || !aligned16(p)) FAIL(HYMBA_ERR_INVALID_ARG, "linear heads' weight pointer null or not 16-byte aligned");
+  layer->linear = *heads;
+  layer->linear_on = true;
+  return HYMBA_OK;
+}
+
+// A consumer reads keys at its producer's positions: both must rotate alike.
+static hymba_status check_rotation(const hymba_layer *layer) {
+  const hymba_layer *p = layer->producer;
+  if (!p || p->id != layer->producer_id) return HYMBA_OK;  // a stale producer is reported by its stamp
+  const hymba_rope a = layer->heads_on ? layer->heads.rope : hymba_rope{}, b = p->heads_on ? p->heads.rope : hymba_rope{};
+  bool same = a.dim == b.dim;
+  if (same && a.dim > 0) {
+    same = a.layout == b.layout && a.scaling == b.scaling && a.base == b.base && a.attn_factor == b.attn_factor;
+    if (same && a.scaling != HYMBA_ROPE_SCALE_NONE) same = a.factor == b.factor;
+    if (same && a.scaling == HYMBA_ROPE_SCALE_WAVELENGTH)
+      same = a.orig_len == b.orig_len && a.low_turns == b.low_turns && a.high_turns == b.high_turns;
+  }
+  if (!same) FAIL(HYMBA_ERR_NOT_BOUND, "producer and consumer rotate their heads differently");
+  return HYMBA_OK;
+}
+
+// Norm and rotation of `nb` sequences' query rows [nb, rows, H, dqk] (row stride ldq) and, for a
+// K/V owner, key rows k, in place, from position pos0 on.
+static hymba_status heads_in_place(const hymba_layer *layer, int nb, int rows, void *q, void *k, int64_t k_batch,
+                                   int64_t k_row, int64_t k_head, int64_t pos0, cudaStream_t s) {
+  const hymba_layer_config &c = layer->cfg;
+  hymba_qk_norm_rope_args a{};
+  a.dtype = c.dtype;
+  a.batch = nb;
+  a.n_rows = rows;
+  a.head_dim = c.head_dim_qk;
+  const int64_t w = qk_width(c);
+  a.q = {q, q, layer->heads.q_weight, rows * w, w, c.head_dim_qk, rows * w, w, c.head_dim_qk, c.n_heads};
+  if (k)
+    a.k = {k, k, layer->heads.k_weight, k_batch, k_row, k_head, k_batch, k_row, k_head, c.n_kv_heads};
+  a.norm = layer->heads.norm;
+  a.eps = layer->heads.eps;
+  a.rope = layer->heads.rope;
+  a.pos0 = pos0;
+  return qk_norm_rope(a, s);
+}
+
+// The linear heads over nb sequences of `rows` rows: u and the gate [nb, rows, E], B and C
+// [nb, rows, 2 N], step sizes and log decays [nb, rows, H].
+static hymba_linear_attention linear_heads_args(const hymba_layer *layer, int nb, int rows, const void *u, const void *z,
+                                                const void *bc, const float *delta, const float *decay, void *y) {
+  const hymba_layer_config &c = layer->cfg;
+  const int64_t E = c.d_inner, N = layer->linear.d_state, H = c.n_heads, dv = c.head_dim_v;
+  hymba_linear_attention a{};
+  a.dtype = c.dtype;
+  a.batch = nb;
+  a.n_rows = rows;
+  a.n_heads = c.n_heads;
+  a.n_qk_heads = 1;
+  a.dk = (int)N;
+  a.dv = c.head_dim_v;
+  a.scale = 1.f;
+  a.k = bc;
+  a.q = bc ? reinterpret_cast<const char *>(bc) + N * esize(c.dtype) : nullptr;
+  a.q_batch = a.k_batch = rows * 2 * N;
+  a.q_row = a.k_row = 2 * N;
+  a.q_head = a.k_head = N;
+  a.v = u;
+  a.gate = z;
+  a.o = y;
+  a.v_batch = a.gate_batch = a.o_batch = rows * E;
+  a.v_row = a.gate_row = a.o_row = E;
+  a.v_head = a.gate_head = a.o_head = dv;
+  a.log_decay = decay;
+  a.in_scale = delta;
+  a.decay_batch = a.scale_batch = rows * H;
+  a.decay_row = a.scale_row = H;
+  a.decay_head = a.scale_head = 1;
+  a.skip = layer->linear.d_skip;
+  return a;
+}
+
+// ---------------------------------------------------------------------------
 // prefill
 // ---------------------------------------------------------------------------
 // Work counters of the persistent kernels in a prefill's workspace (one per launch).
@@ -272,6 +401,19 @@ static void branch_split(const hymba_layer_config &c, int batch, int *n, int *bc
   const int want = c.branch_chunks >= 2 ? std::min(c.branch_chunks, batch) : 1;
   *bc = (batch + want - 1) / want;
   *n = (batch + *bc - 1) / *bc;
+}
+
+// Inside the delta region with linear heads: B and C [M, 2 N] dtype, step sizes and log decays
+// [M, H] fp32.
+struct LinearInputsLayout {
+  size_t bc, delta, decay, total;
+};
+static LinearInputsLayout linear_inputs_layout(const hymba_layer &l, size_t M) {
+  LinearInputsLayout o{};
+  o.delta = up256(M * 2 * l.linear.d_state * esize(l.cfg.dtype));
+  o.decay = o.delta + up256(M * l.cfg.n_heads * 4);
+  o.total = o.decay + up256(M * l.cfg.n_heads * 4);
+  return o;
 }
 
 // Workspace of a prefill whose intermediates have `rows` rows per sequence: all L = m + n
@@ -294,14 +436,18 @@ static hymba_status prefill_layout_rows(const hymba_layer *layer, int batch, lon
   o->x_ssm = take(M * E * es);
   o->gate = take(M * E * es);
   o->u = take(M * E * es);
-  o->xdbl = take(M * xdbl_width(c) * 4);
-  o->delta = take(M * E * es);
+  // linear heads: the padded projection; then B and C, the step sizes and the log decays
+  o->xdbl = take(M * ssm_proj_ld(*layer) * 4);
+  o->delta = take(layer->linear_on ? std::max(M * E * es, linear_inputs_layout(*layer, M).total) : M * E * es);
   o->y_ssm = take(M * E * es);
   o->o_attn = take(M * E * es);
   o->fused = take(M * E * es);
   // the scan's chunk states for the whole batch (a concurrent prefill's batch chunks scan
   // with the whole batch's time chunks, one after another, in the same region)
   size_t sf = scan_workspace_floats(batch, (int)rows, c.d_inner, c.d_state, nullptr);
+  if (layer->linear_on)
+    sf = linear_attention_workspace_bytes(linear_heads_args(layer, batch, (int)rows, nullptr, nullptr, nullptr, nullptr,
+                                                            nullptr, nullptr)) / 4;
   if (scan_floats) *scan_floats = sf;
   take(sf * 4);  // scan chunk states, after `fused`
   // rotary table of the positions 0..L-1 (none without a rotary embedding)
@@ -430,15 +576,22 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
   const long long M = (long long)batch * r.rows;
   const size_t es = esize(c.dtype);
   const int E = c.d_inner;
-  const int XW = xdbl_width(c);
+  const int XW = ssm_proj_width(*layer), XL = ssm_proj_ld(*layer);
+  const bool linear = layer->linear_on;
   hymba_status st;
   if (M > 0x7fffffffLL) FAIL(HYMBA_ERR_UNSUPPORTED, "too many rows");
+  if ((st = check_rotation(layer)) != HYMBA_OK) return st;
 
   char *ws = reinterpret_cast<char *>(workspace);
   void *q = ws + lay.q, *xs = ws + lay.x_ssm, *z = ws + lay.gate, *u = ws + lay.u;
   float *xdbl = reinterpret_cast<float *>(ws + lay.xdbl);
   void *delta = ws + lay.delta, *yssm = ws + lay.y_ssm, *o = ws + lay.o_attn, *f = ws + lay.fused;
   float *scan_ws = reinterpret_cast<float *>(ws + lay.fused + up256((size_t)M * E * es));
+  LinearInputsLayout li{};
+  if (linear) li = linear_inputs_layout(*layer, (size_t)M);
+  char *lin_bc = ws + lay.delta + li.bc;
+  float *lin_delta = reinterpret_cast<float *>(ws + lay.delta + li.delta);
+  float *lin_decay = reinterpret_cast<float *>(ws + lay.delta + li.decay);
   // work counters of this call's persistent GEMMs, one per launch
   unsigned *sched = reinterpret_cast<unsigned *>(ws + lay.sched);
   int next_ctr = 0;
@@ -488,7 +641,12 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
       if (!consumer) g.epi.seg[1].rope = 1;
     }
     g.tile_ctr = take_ctr();
-    return gemm(g, c.dtype, s);
+    hymba_status gst = gemm(g, c.dtype, s);
+    if (gst != HYMBA_OK || !layer->heads_on) return gst;
+    // norm and rotation of the heads just projected, keys in their rows of the K/V sequence
+    return heads_in_place(layer, nb, r.rows, elem_at(q, m0 * qk_width(c), es),
+                          consumer ? nullptr : elem_at(kv->k, ((long long)b0 * L + r.q_off) * k_width(c), es),
+                          (int64_t)L * k_width(c), k_width(c), c.head_dim_qk, r.q_off, s);
   };
   // 2. causal conv + SiLU -> u (and the conv state)
   auto conv = [&](int b0, int nb, cudaStream_t s) -> hymba_status {
@@ -515,13 +673,13 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
     GemmArgs g{};
     g.A = elem_at(u, m0 * E, es);
     g.lda = E;
-    g.B = layer->w.w_x;
+    g.B = linear ? layer->linear.w_x : layer->w.w_x;
     g.ldb = E;
     g.M = (int)((long long)nb * r.rows);
     g.N = XW;
     g.K = E;
     g.elem = (int)es;
-    g.epi.seg[0] = seg(xdbl + m0 * XW, XW, 0, XW, 1, es);
+    g.epi.seg[0] = seg(xdbl + m0 * XL, XL, 0, XW, 1, es, 0, linear ? XL : 0);
     g.epi.nseg = 1;
     g.tile_ctr = take_ctr();
     return gemm(g, c.dtype, s);
@@ -530,6 +688,20 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
   auto dt_proj = [&](int b0, int nb, cudaStream_t s) -> hymba_status {
     ProfScope prof_scope(s, step_name(r, 3));
     const long long m0 = (long long)b0 * r.rows;
+    if (linear) {  // one step size and log decay for each head instead
+      LinearInputsArgs a{};
+      a.raw = xdbl + m0 * XL;
+      a.ld_raw = XL;
+      a.b_dt = layer->linear.b_dt;
+      a.a_log = layer->linear.a_log;
+      a.bc = lin_bc + m0 * 2 * layer->linear.d_state * es;
+      a.delta = lin_delta + m0 * c.n_heads;
+      a.decay = lin_decay + m0 * c.n_heads;
+      a.M = (long long)nb * r.rows;
+      a.N = layer->linear.d_state;
+      a.H = c.n_heads;
+      return linear_inputs(a, c.dtype, s);
+    }
     GemmArgs g{};
     g.A = xdbl + m0 * XW;
     g.lda = XW;
@@ -550,6 +722,14 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
   auto scan = [&](int b0, int nb, cudaStream_t s) -> hymba_status {
     ProfScope prof_scope(s, step_name(r, 4));
     const long long m0 = (long long)b0 * r.rows;
+    if (linear) {
+      hymba_linear_attention a = linear_heads_args(
+          layer, nb, r.rows, elem_at(u, m0 * E, es), elem_at(z, m0 * E, es), lin_bc + m0 * 2 * layer->linear.d_state * es,
+          lin_delta + m0 * c.n_heads, lin_decay + m0 * c.n_heads, elem_at(yssm, m0 * E, es));
+      a.state_in = r.h0;  // one for every sequence
+      a.state_out = ssm_cache ? ssm_cache->h + (long long)b0 * E * ssm_states(*layer) : nullptr;
+      return linear_attention(a, scan_ws, s, batch);
+    }
     ScanArgs a{};
     a.u = elem_at(u, m0 * E, es);
     a.delta = elem_at(delta, m0 * E, es);
@@ -899,10 +1079,11 @@ hymba_status hymba_layer_prefill_cached(hymba_layer *layer, int batch, int n_tok
 // decode
 // ---------------------------------------------------------------------------
 struct DecodeLayout {
-  size_t q, x_ssm, z, u, xacc, y_ssm, o, f, part, rope, total;
+  size_t q, x_ssm, z, u, xacc, linear, y_ssm, o, f, part, rope, total;
 };
 
-static DecodeLayout decode_layout(const hymba_layer_config &c, int batch, long long pos) {
+static DecodeLayout decode_layout(const hymba_layer &layer, int batch, long long pos) {
+  const hymba_layer_config &c = layer.cfg;
   DecodeLayout d{};
   const size_t es = esize(c.dtype), E = c.d_inner, B = batch;
   size_t off = 0;
@@ -915,7 +1096,8 @@ static DecodeLayout decode_layout(const hymba_layer_config &c, int batch, long l
   d.x_ssm = take(B * E * es);
   d.z = take(B * E * es);
   d.u = take(B * E * es);
-  d.xacc = take(B * xdbl_width(c) * 8 + B * 4);  // x_proj result as 64-bit fixed point, then [B] flags
+  d.xacc = take(B * ssm_proj_width(layer) * 8 + B * 4);  // x_proj result as 64-bit fixed point, then [B] flags
+  d.linear = take(layer.linear_on ? linear_inputs_layout(layer, B).total : 0);
   d.y_ssm = take(B * E * es);
   d.o = take(B * E * es);
   d.f = take(B * E * es);
@@ -934,7 +1116,7 @@ hymba_status hymba_layer_decode_workspace(const hymba_layer *layer, int batch, i
   if (max_pos < c.n_meta) FAIL(HYMBA_ERR_INVALID_ARG, "max_pos %lld is a meta position", (long long)max_pos);
   if (c.is_global && max_pos >= (1LL << 24)) FAIL(HYMBA_ERR_UNSUPPORTED, "max_pos beyond 2^24");
   // the workspace grows with the number of visible keys, which never falls as pos grows
-  *bytes = decode_layout(c, batch, max_pos).total;
+  *bytes = decode_layout(*layer, batch, max_pos).total;
   return HYMBA_OK;
 }
 
@@ -965,9 +1147,10 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
     FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache belongs to another layer");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     FAIL(HYMBA_ERR_INVALID_ARG, "workspace null or not 256-byte aligned");
-  const DecodeLayout d = decode_layout(c, batch, pos);
+  const DecodeLayout d = decode_layout(*layer, batch, pos);
   if (workspace_bytes < d.total)
     FAIL(HYMBA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, d.total);
+  if (hymba_status rst = check_rotation(layer); rst != HYMBA_OK) return rst;
 
   const size_t es = esize(c.dtype);
   const int E = c.d_inner;
@@ -982,7 +1165,7 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
   // the step's kernels are launched programmatically: each starts while its predecessor ends
   PdlScope pdl;
 
-  const long long xacc_n = (long long)batch * xdbl_width(c);
+  const long long xacc_n = (long long)batch * ssm_proj_width(*layer);
   unsigned *xbad = reinterpret_cast<unsigned *>(xacc + xacc_n);
   bool xacc_zeroed = false;
   // 1. input projection; a K/V owner writes this token's K/V straight into its slot
@@ -1020,6 +1203,11 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
       xacc_zeroed = true;
     }
     if ((st = gemm_decode(g, c.dtype, stream)) != HYMBA_OK) return st;
+    // norm and rotation of the new token's heads, its key in its slot
+    if (layer->heads_on &&
+        (st = heads_in_place(layer, batch, 1, q, consumer ? nullptr : kbase, (int64_t)c.n_kv_heads * cap * c.head_dim_qk,
+                             c.head_dim_qk, cap * c.head_dim_qk, pos, stream)) != HYMBA_OK)
+      return st;
   }
   // The two branches side by side when the handle has a side stream (branch_chunks >= 2):
   // the SSM branch there, at the highest priority (short launches), beside the attention.
@@ -1062,8 +1250,36 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
     if (!xacc_zeroed &&
         cudaMemsetAsync(xacc, 0, (size_t)xacc_n * sizeof(long long) + (size_t)batch * 4, ssm_stream) != cudaSuccess)
       FAIL(HYMBA_ERR_CUDA, "cudaMemsetAsync(x_proj accumulator): %s", cudaGetErrorString(cudaGetLastError()));
+    if (layer->linear_on) {
+      a.linear = 1;
+      a.w_x = layer->linear.w_x;
+      a.R = c.n_heads;
+      a.N = layer->linear.d_state;
+    }
     if ((st = decode_conv_xproj(a, c.dtype, ssm_stream)) != HYMBA_OK) return st;
-    if ((st = decode_scan(a, c.dtype, ssm_stream)) != HYMBA_OK) return st;
+    if (layer->linear_on) {
+      const LinearInputsLayout li = linear_inputs_layout(*layer, batch);
+      LinearInputsArgs x{};
+      x.raw = xacc;
+      x.ld_raw = ssm_proj_width(*layer);
+      x.fixed = 1;
+      x.bad = xbad;
+      x.b_dt = layer->linear.b_dt;
+      x.a_log = layer->linear.a_log;
+      x.bc = ws + d.linear + li.bc;
+      x.delta = reinterpret_cast<float *>(ws + d.linear + li.delta);
+      x.decay = reinterpret_cast<float *>(ws + d.linear + li.decay);
+      x.M = batch;
+      x.N = layer->linear.d_state;
+      x.H = c.n_heads;
+      if ((st = linear_inputs(x, c.dtype, ssm_stream)) != HYMBA_OK) return st;
+      hymba_linear_attention step = linear_heads_args(layer, batch, 1, u, z, x.bc, x.delta, x.decay, yssm);
+      step.state_in = step.state_out = ssm_cache->h;
+      step.state_in_batch = (int64_t)E * layer->linear.d_state;
+      if ((st = linear_attention_step(step, ssm_stream)) != HYMBA_OK) return st;
+    } else if ((st = decode_scan(a, c.dtype, ssm_stream)) != HYMBA_OK) {
+      return st;
+    }
   }
   if (side_by_side && cudaEventRecord(br.ev[1], br.side) != cudaSuccess)
     FAIL(HYMBA_ERR_CUDA, "decode join: %s", cudaGetErrorString(cudaGetLastError()));
@@ -1303,7 +1519,7 @@ hymba_status hymba_block_decode_step(hymba_layer *layer, const hymba_block_weigh
   if (st != HYMBA_OK) return st;
   const hymba_layer_config &c = layer->cfg;
   if (batch < 1 || pos < c.n_meta) FAIL(HYMBA_ERR_INVALID_ARG, "batch < 1 or pos is a meta position");
-  const size_t mixer = decode_layout(c, batch, pos).total;
+  const size_t mixer = decode_layout(*layer, batch, pos).total;
   const BlockLayout bl = block_layout(mixer, c, batch, bw->mlp_hidden);
   if (!x_t || !y_t || !aligned16(x_t) || !aligned16(y_t) || x_t == y_t)
     FAIL(HYMBA_ERR_INVALID_ARG, "x_t/y_t null, misaligned or the same");

@@ -290,6 +290,7 @@ struct DecodeSsmArgs {
   float *h;            // [B, E, N] fp32 state, updated in place
   void *y;             // [B, E] gated output
   int B, E, K, R, N;
+  int linear;          // the x_proj rows feed linear heads (N of them B and C each, R deltas), not decode_scan
 };
 // u = SiLU(conv(window, x) + b), the conv window advanced in place, and x_proj:
 // xacc += u W_x^T per channel block, in fixed point (xacc zeroed beforehand).
@@ -301,8 +302,24 @@ hymba_status decode_scan(const DecodeSsmArgs &a, hymba_dtype dt, cudaStream_t s)
 hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s);
 // One row per sequence (a.n_rows == 1).
 hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s);
-// Whole sequences; workspace of linear_attention_workspace_bytes(a) bytes.
-hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s);
+// Whole sequences; workspace of linear_attention_workspace_bytes(a) bytes.  `whole_batch`: the
+// batch that this call is a part of, whose split of the rows and workspace size it takes (so
+// that every part rounds alike); 0: a.batch.
+hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s, int whole_batch = 0);
+// The linear heads' inputs from their projection [B, C, d] of M rows: `raw` fp32 rows ld_raw
+// apart, or (fixed) the decode step's 64-bit fixed-point sums with the rows' flags.
+struct LinearInputsArgs {
+  const void *raw;
+  long long ld_raw;
+  int fixed;
+  const unsigned *bad;        // fixed: rows whose sums were not finite
+  const float *b_dt, *a_log;  // [H]
+  void *bc;                   // [M, 2 N] dtype: B, C
+  float *delta, *decay;       // [M, H]: softplus(d + b_dt), -exp(a_log) delta
+  long long M;
+  int N, H;
+};
+hymba_status linear_inputs(const LinearInputsArgs &a, hymba_dtype dt, cudaStream_t s);
 // The rows of few heads split into segments: pass 0 computes each segment's own state (from
 // zero, the first from the call's) and the sum of its log decays, all but the last one's;
 // pass 1 the outputs, each segment from the states before it.  n = 1: pass 1 alone.

@@ -391,11 +391,13 @@ size_t linear_attention_workspace_bytes(const hymba_linear_attention &a) {
   return g.n > 1 ? segment_state_bytes(a, g) + (size_t)g.n * a.batch * a.n_heads * 8 : 0;
 }
 
-hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s) {
-  LinearSegments g = segments_of(a);
+hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s, int whole_batch) {
+  hymba_linear_attention whole = a;
+  if (whole_batch > 0) whole.batch = whole_batch;
+  LinearSegments g = segments_of(whole);
   if (g.n > 1) {
     g.state = reinterpret_cast<float *>(workspace);
-    g.decay = reinterpret_cast<double *>(reinterpret_cast<char *>(workspace) + segment_state_bytes(a, g));
+    g.decay = reinterpret_cast<double *>(reinterpret_cast<char *>(workspace) + segment_state_bytes(whole, g));
   }
   if (on_tensor_cores(a)) return linear_attention_tc(a, g, s);
   if (a.dtype == HYMBA_BF16) scan_launch<__nv_bfloat16>(a, g, s);

@@ -549,7 +549,8 @@ static hymba_status decode_scan_t(const DecodeSsmArgs &a, cudaStream_t s) {
 
 static hymba_status decode_check(const DecodeSsmArgs &a, hymba_dtype dt) {
   const int V = dt == HYMBA_BF16 ? 8 : 4;
-  if (a.N != kStates || a.K > 4 || a.K < 1 || a.E % kScanCh || a.E % V || a.R % 4) {
+  const bool scan_ok = a.linear || (a.N == kStates && a.R % 4 == 0);
+  if (!scan_ok || a.K > 4 || a.K < 1 || a.E % kScanCh || a.E % V) {
     set_error("decode SSM needs d_state 16, 1 <= d_conv <= 4, d_inner %% 32 == 0, dt_rank %% 4 == 0");
     return HYMBA_ERR_UNSUPPORTED;
   }
@@ -583,6 +584,46 @@ hymba_status decode_scan(const DecodeSsmArgs &a, hymba_dtype dt, cudaStream_t s)
   st = dt == HYMBA_BF16 ? decode_scan_t<__nv_bfloat16>(a, s) : decode_scan_t<float>(a, s);
   if (st != HYMBA_OK) return st;
   return launched("scan step");
+}
+
+// ---------------------------------------------------------------------------
+// linear heads: B, C, step sizes and log decays from their projection
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) linear_inputs_kernel(LinearInputsArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int NJ = 2 * a.N + a.H;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * NJ) return;
+  const long long m = i / NJ;
+  const int j = int(i - m * NJ);
+  float v;
+  if (a.fixed) {
+    v = __ll2float_rn(reinterpret_cast<const long long *>(a.raw)[m * a.ld_raw + j]) * kXprojUnfix;
+    if (a.bad[m]) v = __int_as_float(0x7fc00000);
+  } else {
+    v = reinterpret_cast<const float *>(a.raw)[m * a.ld_raw + j];
+  }
+  if (j < 2 * a.N) {
+    reinterpret_cast<T *>(a.bc)[m * 2 * a.N + j] = Store<T>::from_f(v);
+  } else {
+    const int h = j - 2 * a.N;
+    const float d = softplus_accurate(v + a.b_dt[h]);
+    a.delta[m * a.H + h] = d;
+    a.decay[m * a.H + h] = -expf(a.a_log[h]) * d;
+  }
+}
+
+hymba_status linear_inputs(const LinearInputsArgs &a, hymba_dtype dt, cudaStream_t s) {
+  const long long blocks = (a.M * (2 * a.N + a.H) + 255) / 256;
+  if (blocks > 0x7fffffffLL) {
+    set_error("too many rows");
+    return HYMBA_ERR_UNSUPPORTED;
+  }
+  if (dt == HYMBA_BF16) launch_kernel(linear_inputs_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+  else launch_kernel(linear_inputs_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return launched("linear heads' inputs");
 }
 
 // ---------------------------------------------------------------------------

@@ -502,6 +502,48 @@ HYMBA_API hymba_status hymba_linear_attention_prefill(const hymba_linear_attenti
 HYMBA_API hymba_status hymba_linear_attention_decode_step(const hymba_linear_attention *args,
                                                           hymba_stream_t stream);
 
+/* ---- operators inside the layer ------------------------------------------------- */
+
+/* Norm and rotation of the layer's query and key heads (hymba_qk_norm_rope) between the input
+ * projection and the attention, in every later prefill, meta precompute and decode call of the
+ * handle, blocks included: row p of X~ is at position p, so the K/V sequence and the decode
+ * store hold normed and rotated keys.  A K/V-sharing consumer applies its own to its queries
+ * (k_weight unused) and must be given its producer's rotation (NOT_BOUND at the call
+ * otherwise).  The weight pointers are kept by the handle until destroy or the next set.
+ * head_dim_qk must be a multiple of 8; rope.dim > 0 excludes the configuration's rope_base. */
+typedef struct {
+  int norm;
+  float eps;
+  const float *q_weight; /* [head_dim_qk] or NULL */
+  const float *k_weight; /* [head_dim_qk] or NULL */
+  hymba_rope rope;
+} hymba_layer_heads;
+/* NULL: back to the heads as projected.  Host only; no call on the handle may be running. */
+HYMBA_API hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *heads);
+
+/* The SSM branch with linear heads: hymba_linear_attention in place of the selective scan, the
+ * Mamba2-heads variant of the layer (OpenReview reply on Mamba2 heads), n_heads heads of
+ * head_dim_v channels with one step size and one decay each, B and C shared by all of them:
+ *     [B, C, d] = u W_x^T,  delta = softplus(d + b_dt),  g = -exp(a_log) delta   (per head)
+ *     S_t = exp(g_t) S_{t-1} + delta_t u_t B_t^T,   y = (S C + D u) SiLU(z)
+ * for every later call of the handle.  The state in hymba_ssm_cache.h and hymba_meta_cache.h is
+ * then [.., d_inner, d_state] with this d_state, and the configuration's d_state, dt_rank and
+ * the weights w_x, w_dt, b_dt, a_log, d_skip are not used.  In the prefill workspace the
+ * regions xdbl and delta hold other intermediates.
+ *   w_x     [2 * d_state + n_heads, d_inner] dtype; rows: B, C, then one delta per head
+ *   b_dt, a_log  [n_heads];  d_skip [d_inner] D
+ * d_state a multiple of 8 up to 128; head_dim_v a multiple of 8.  Pointers kept as above. */
+typedef struct {
+  int d_state;
+  const void *w_x;
+  const float *b_dt;
+  const float *a_log;
+  const float *d_skip;
+} hymba_linear_heads;
+/* NULL: back to the selective scan.  Host only; no call on the handle may be running.
+ * Workspace sizes change: query them after the set. */
+HYMBA_API hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hymba_linear_heads *heads);
+
 /* ---- status and diagnostics -------------------------------------------- */
 
 /* Synchronises `stream`, then reports a pending CUDA error or a device-side

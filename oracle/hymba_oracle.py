@@ -223,6 +223,61 @@ def ssm_inputs(u: np.ndarray, w_x: np.ndarray, w_dt: np.ndarray, b_dt: np.ndarra
     return delta, Bm, Cm
 
 
+def heads_norm_rope(x, positions, head_dim: int, heads: dict, weight) -> np.ndarray:
+    """x [rows, n_heads*head_dim] at X~ positions [rows]: every head divided by its rms and scaled by
+    `weight` (norm), then its first rope_dim elements rotated by position * f_i, pairs (2i, 2i+1) or
+    halves (i, i + rope_dim/2).  f_i = base^(-2i/rope_dim), divided by factor ("linear"), or by a
+    mixture of 1 and factor set by the turns over orig_len ("wavelength")."""
+    y = x.reshape(x.shape[0], -1, head_dim).copy()
+    if heads.get("norm"):
+        y = rms_normalise(y, heads["eps"])
+        if weight is not None:
+            y = y * weight
+    rot = heads.get("rope_dim", 0)
+    for i in range(rot // 2):
+        f = heads["base"] ** (-2.0 * i / rot)
+        if heads.get("scaling") == "linear":
+            f /= heads["factor"]
+        elif heads.get("scaling") == "wavelength":
+            turns = heads["orig_len"] * f / (2 * np.pi)
+            keep = np.clip((turns - heads["low_turns"]) / (heads["high_turns"] - heads["low_turns"]), 0, 1)
+            f = keep * f + (1 - keep) * f / heads["factor"]
+        a, b = (2 * i, 2 * i + 1) if heads["layout"] == "pairs" else (i, i + rot // 2)
+        z = (y[:, :, a] + 1j * y[:, :, b]) * heads.get("attn_factor", 1.0) * np.exp(
+            1j * np.asarray(positions, dtype=np.float64) * f)[:, None]
+        y[:, :, a], y[:, :, b] = z.real, z.imag
+    return y.reshape(x.shape[0], -1)
+
+
+def _place_heads(q, k, positions, w: dict, s: "Spec", consumer: bool):
+    """Queries and keys at their positions: rope_base's rotation, or the layer's heads (w["heads"])."""
+    if s.rope_base > 0:
+        q = rope(q, positions, s.head_dim_qk, s.rope_base)
+        if not consumer:
+            k = rope(k, positions, s.head_dim_qk, s.rope_base)
+    if "heads" in w:
+        h = w["heads"]
+        q = heads_norm_rope(q, positions, s.head_dim_qk, h, h.get("q_weight"))
+        if not consumer:
+            k = heads_norm_rope(k, positions, s.head_dim_qk, h, h.get("k_weight"))
+    return q, k
+
+
+def _ssm_terms(u, w: dict, s: "Spec"):
+    """delta [L, E], B, C [L, N], A [E, N] and D [E] of the recurrence; with linear heads
+    (w["linear"]) one delta and one A for all channels and states of a head."""
+    if "linear" not in w:
+        delta, Bm, Cm = ssm_inputs(u, _f64(w["w_x"]), _f64(w["w_dt"]), _f64(w["b_dt"]), s)
+        return delta, Bm, Cm, -np.exp(_f64(w["a_log"])), _f64(w["d_skip"])
+    lw = w["linear"]
+    proj = u @ _f64(lw["w_x"]).T
+    n = (proj.shape[1] - s.n_heads) // 2
+    delta = softplus(proj[:, 2 * n:] + _f64(lw["b_dt"]))
+    spread = s.d_inner // s.n_heads
+    A = np.repeat(-np.exp(_f64(lw["a_log"])), spread)[:, None] * np.ones((1, n))
+    return np.repeat(delta, spread, axis=1), proj[:, :n], proj[:, n:2 * n], A, _f64(lw["d_skip"])
+
+
 def selective_scan(u, delta, A, Bm, Cm, D, h0=None):
     """h_t = exp(delta_t A) * h_{t-1} + delta_t B_t u_t (h_{-1} = h0 or 0);
     y_t = C_t . h_t + D u_t.  Shapes: u, delta [T, E]; A [E, N]; B, C [T, N]; D [E].
@@ -292,17 +347,13 @@ def layer_prefill(xt, w: dict, s: Spec, kv_from: dict | None = None, capacity: i
     L = xt.shape[0]
     consumer = kv_from is not None
     q, k, v, xs, z = in_proj(xt, _f64(w["w_in"]), s, consumer)
-    if s.rope_base > 0:
-        q = rope(q, np.arange(L), s.head_dim_qk, s.rope_base)
-        if not consumer:
-            k = rope(k, np.arange(L), s.head_dim_qk, s.rope_base)
+    q, k = _place_heads(q, k, np.arange(L), w, s, consumer)
     if consumer:
         k, v = kv_from["k"], kv_from["v"]
     o = attention(q, k, v, s)
     u = causal_conv_silu(xs, _f64(w["conv_w"]), _f64(w["conv_b"]))
-    delta, Bm, Cm = ssm_inputs(u, _f64(w["w_x"]), _f64(w["w_dt"]), _f64(w["b_dt"]), s)
-    A = -np.exp(_f64(w["a_log"]))
-    y, hL = selective_scan(u, delta, A, Bm, Cm, _f64(w["d_skip"]))
+    delta, Bm, Cm, A, D = _ssm_terms(u, w, s)
+    y, hL = selective_scan(u, delta, A, Bm, Cm, D)
     y_ssm = y * silu(z)
     f = fuse(o, y_ssm, _f64(w["beta_attn"]), _f64(w["beta_ssm"]), s.eps)
     Y = f @ _f64(w["w_out"]).T
@@ -337,10 +388,7 @@ def layer_decode(x_t, pos: int, w: dict, s: Spec, cache: dict, kv_cache: dict | 
     x_t = _f64(x_t)[None, :]
     consumer = kv_cache is not None
     q, k, v, xs, z = in_proj(x_t, _f64(w["w_in"]), s, consumer)
-    if s.rope_base > 0:
-        q = rope(q, np.array([pos]), s.head_dim_qk, s.rope_base)
-        if not consumer:
-            k = rope(k, np.array([pos]), s.head_dim_qk, s.rope_base)
+    q, k = _place_heads(q, k, np.array([pos]), w, s, consumer)
     new = {key: _f64(val).copy() for key, val in cache.items()}
     if consumer:
         kc, vc = _f64(kv_cache["k"]), _f64(kv_cache["v"])
@@ -367,9 +415,8 @@ def layer_decode(x_t, pos: int, w: dict, s: Spec, cache: dict, kv_cache: dict | 
     hist = new["conv"]
     u = causal_conv_silu(xs, _f64(w["conv_w"]), _f64(w["conv_b"]), history=hist)
     new["conv"] = np.concatenate([hist[1:], xs], axis=0)
-    delta, Bm, Cm = ssm_inputs(u, _f64(w["w_x"]), _f64(w["w_dt"]), _f64(w["b_dt"]), s)
-    A = -np.exp(_f64(w["a_log"]))
-    y, h1 = selective_scan(u, delta, A, Bm, Cm, _f64(w["d_skip"]), h0=new["ssm"])
+    delta, Bm, Cm, A, D = _ssm_terms(u, w, s)
+    y, h1 = selective_scan(u, delta, A, Bm, Cm, D, h0=new["ssm"])
     new["ssm"] = h1
     y_ssm = y * silu(z)
     f = fuse(o, y_ssm, _f64(w["beta_attn"]), _f64(w["beta_ssm"]), s.eps)

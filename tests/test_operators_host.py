@@ -186,3 +186,82 @@ def test_plain_rotation_is_a_complex_product():
             z = torch.complex(x[..., a], x[..., b]) * turn
             torch.testing.assert_close(torch.complex(y[..., a], y[..., b]), z, rtol=1e-12, atol=1e-12)
         torch.testing.assert_close(y[..., 6:], x[..., 6:], rtol=0, atol=0)
+
+
+def _layer(**kw):
+    base = dict(d_model=256, n_heads=4, n_kv_heads=2, head_dim_qk=64, d_inner=512, d_state=16, d_conv=4, dt_rank=16,
+                n_meta=16, window=64, is_global=False, dtype="bf16")
+    base.update(kw)
+    return hy.hymba_layer_create(hy.make_config(**base), hy.hymba_layer_weights(*[A + 4096 * i for i in range(11)]))
+
+
+@pytest.mark.parametrize("heads,cfg,status", [
+    (dict(rope=hy.make_rope(66)), {}, hy.HYMBA_ERR_INVALID_ARG),
+    (dict(rope=hy.make_rope(64, base=0.5)), {}, hy.HYMBA_ERR_INVALID_ARG),
+    (dict(rope=hy.make_rope(64)), dict(rope_base=10000.0), hy.HYMBA_ERR_INVALID_ARG),
+    (dict(eps=-1.0), {}, hy.HYMBA_ERR_INVALID_ARG),
+    (dict(norm=False, q_weight=A), {}, hy.HYMBA_ERR_INVALID_ARG),
+    (dict(k_weight=A + 4), {}, hy.HYMBA_ERR_INVALID_ARG),
+    ({}, dict(dtype="f32", head_dim_qk=20), hy.HYMBA_ERR_UNSUPPORTED),
+])
+def test_layer_heads_refuse(heads, cfg, status):
+    h = _layer(**cfg)
+    with pytest.raises(hy.HymbaError) as e:
+        hy.hymba_layer_set_heads(h, hy.make_layer_heads(**heads))
+    assert e.value.status == status
+    hy.hymba_layer_set_heads(h, None)
+    hy.hymba_layer_destroy(h)
+    with pytest.raises(hy.HymbaError):
+        hy.hymba_layer_set_heads(None, None)
+
+
+@pytest.mark.parametrize("d_state,missing,status", [
+    (0, None, hy.HYMBA_ERR_UNSUPPORTED), (20, None, hy.HYMBA_ERR_UNSUPPORTED), (136, None, hy.HYMBA_ERR_UNSUPPORTED),
+    (64, "b_dt", hy.HYMBA_ERR_INVALID_ARG), (64, "w_x", hy.HYMBA_ERR_INVALID_ARG)])
+def test_linear_heads_refuse(d_state, missing, status):
+    h = _layer()
+    before = hy.hymba_layer_prefill_workspace(h, 2, 100), hy.hymba_layer_decode_workspace(h, 2, 100)
+    w = {n: A + 4096 * i for i, n in enumerate(("w_x", "b_dt", "a_log", "d_skip"))}
+    if missing:
+        w[missing] = None
+    with pytest.raises(hy.HymbaError) as e:
+        hy.hymba_layer_set_linear_heads(h, hy.make_linear_heads(w, d_state))
+    assert e.value.status == status
+    assert before == (hy.hymba_layer_prefill_workspace(h, 2, 100), hy.hymba_layer_decode_workspace(h, 2, 100))
+    good = {n: A + 4096 * i for i, n in enumerate(("w_x", "b_dt", "a_log", "d_skip"))}
+    hy.hymba_layer_set_linear_heads(h, hy.make_linear_heads(good, 128))
+    assert hy.hymba_layer_decode_workspace(h, 2, 100) > before[1]
+    hy.hymba_layer_set_linear_heads(h, None)
+    assert before == (hy.hymba_layer_prefill_workspace(h, 2, 100), hy.hymba_layer_decode_workspace(h, 2, 100))
+    hy.hymba_layer_destroy(h)
+
+
+def test_oracle_heads_and_linear_heads_against_the_plain_forms():
+    """The layer oracle's versions of both operators agree with the ones written for the operators'
+    tests, and its rotation with the configuration's own where they overlap."""
+    import numpy as np
+    from oracle import hymba_oracle as O
+    from tests import _small as T
+    r = np.random.default_rng(2)
+    x, pos = r.normal(size=(5, 3 * 8)), np.array([0, 1, 7, 300, 8191])
+    np.testing.assert_allclose(O.heads_norm_rope(x, pos, 8, dict(rope_dim=8, base=100.0, layout="pairs"), None),
+                               O.rope(x, pos, 8, 100.0), rtol=1e-12, atol=1e-12)
+    wl = dict(scaling="wavelength", factor=4.0, orig_len=512.0, low_turns=1.0, high_turns=4.0)
+    w = r.normal(size=8)
+    got = O.heads_norm_rope(x, pos, 8, dict(norm=True, eps=1e-5, rope_dim=6, base=50.0, layout="halves", attn_factor=1.2, **wl), w)
+    want, _ = P.heads(torch.tensor(x).view(1, 5, 3, 8), torch.tensor(w), True, 1e-5, torch.tensor(pos)[None], 6, "halves",
+                      1.2, P.frequencies(6, 50.0, **wl))
+    np.testing.assert_allclose(got, want.view(5, 24).numpy(), rtol=1e-11, atol=1e-12)
+    s = T.spec()
+    E, nh, n, L = s.d_inner, s.n_heads, 6, 9
+    u = r.normal(size=(L, E))
+    lw = dict(w_x=r.normal(size=(2 * n + nh, E)) / 4, b_dt=r.normal(size=nh), a_log=r.normal(size=nh), d_skip=r.normal(size=E))
+    y, h = O.selective_scan(u, *O._ssm_terms(u, dict(linear=lw), s))
+    proj = torch.tensor(u @ lw["w_x"].T)
+    delta = torch.nn.functional.softplus(proj[:, 2 * n:] + torch.tensor(lw["b_dt"]))
+    t = lambda a: a[None, :, None]  # noqa: E731
+    o, S, _, _ = P.linear(t(proj[:, n:2 * n]), t(proj[:, :n]), torch.tensor(u).view(1, L, nh, E // nh),
+                          torch.zeros(1, L, nh, E // nh), (-torch.tensor(lw["a_log"]).exp() * delta)[None], delta[None],
+                          skip=torch.tensor(lw["d_skip"]).view(nh, -1))
+    np.testing.assert_allclose(y, o.view(L, E).numpy(), rtol=1e-10, atol=1e-12)
+    np.testing.assert_allclose(h, S.view(E, n).numpy(), rtol=1e-10, atol=1e-12)
