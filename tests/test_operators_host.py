@@ -256,7 +256,8 @@ def test_oracle_heads_and_linear_heads_against_the_plain_forms():
     E, nh, n, L = s.d_inner, s.n_heads, 6, 9
     u = r.normal(size=(L, E))
     lw = dict(w_x=r.normal(size=(2 * n + nh, E)) / 4, b_dt=r.normal(size=nh), a_log=r.normal(size=nh), d_skip=r.normal(size=E))
-    y, h = O.selective_scan(u, *O._ssm_terms(u, dict(linear=lw), s))
+    spread, Bm, Cm, A_, D = O._ssm_terms(u, dict(linear=lw), s)
+    y, h = O.selective_scan(u, spread, A_, Bm, Cm, D)
     proj = torch.tensor(u @ lw["w_x"].T)
     delta = torch.nn.functional.softplus(proj[:, 2 * n:] + torch.tensor(lw["b_dt"]))
     t = lambda a: a[None, :, None]  # noqa: E731
