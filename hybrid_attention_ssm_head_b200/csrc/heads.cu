@@ -10,7 +10,7 @@ namespace hymba {
 
 namespace {
 
-constexpr int kHeadWarps = 8;
+constexpr int kHeadWarps = 4;
 constexpr int kAhead = 4;
 constexpr int kMaxPairs = 128;  // head_dim <= 256
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -20,7 +20,7 @@ struct HeadsParams {
   int lanes;       // lanes per head: a power of two, 8 elements each
   int parts;       // units per row: the heads of a row are split over this many warps
   int chunk;       // loads (of 32 / lanes heads) a warp keeps in flight, at most kAhead
-  long long units; // batch * n_rows * parts
+  unsigned units;  // batch * n_rows * parts
   double turns[kMaxPairs];  // f_i / (2 pi): turns per position
 };
 
@@ -30,18 +30,22 @@ struct Vec4;
 template <>
 struct Vec4<__nv_bfloat16> {
   using R = uint2;
-  static __device__ __forceinline__ void get(const R &r, float *x) {
-    x[0] = bf16_lo(r.x), x[1] = bf16_hi(r.x), x[2] = bf16_lo(r.y), x[3] = bf16_hi(r.y);
+  static __device__ __forceinline__ void get(const R &r, float2 *x) {
+    x[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+    x[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
   }
-  static __device__ __forceinline__ R put(const float *x) {
-    return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  static __device__ __forceinline__ R put(const float2 *x) {
+    return make_uint2(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y));
   }
 };
 template <>
 struct Vec4<float> {
   using R = float4;
-  static __device__ __forceinline__ void get(const R &r, float *x) { x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w; }
-  static __device__ __forceinline__ R put(const float *x) { return make_float4(x[0], x[1], x[2], x[3]); }
+  static __device__ __forceinline__ void get(const R &r, float2 *x) {
+    x[0] = make_float2(r.x, r.y);
+    x[1] = make_float2(r.z, r.w);
+  }
+  static __device__ __forceinline__ R put(const float2 *x) { return make_float4(x[0].x, x[0].y, x[1].x, x[1].y); }
 };
 
 // Which eight elements of a head a lane holds, and where an element's pair is.
@@ -72,17 +76,24 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   __shared__ float s_stage[PARTNER == kShared ? kHeadWarps * 256 : 1];
   const hymba_qk_norm_rope_args &a = p.a;
   const int warp = warp_id(), lane = lane_id();
-  const long long unit = (long long)blockIdx.x * kHeadWarps + warp;
+  const unsigned unit = blockIdx.x * kHeadWarps + warp;
   if (unit >= p.units) return;
-  const int part = int(unit % p.parts);
-  const long long row_id = unit / p.parts;
-  const int r = int(row_id % a.n_rows);
-  const long long b = row_id / a.n_rows;
+  const unsigned row_id = p.parts == 1 ? unit : unit / (unsigned)p.parts;
+  const int part = int(unit - row_id * p.parts);
+  const int b = int(row_id / (unsigned)a.n_rows), r = int(row_id - b * (unsigned)a.n_rows);
   const int lanes = p.lanes, li = lane & (lanes - 1), slot = lane / lanes, per = 32 / lanes;
   const int d = a.head_dim, rot = a.rope.dim, half = rot >> 1;
   const bool live = 8 * li < d;
   // the lane's elements: four from e0, four from e1
   const int e0 = PARTNER == kHalves ? 4 * li : 8 * li, e1 = PARTNER == kHalves ? half + 4 * li : e0 + 4;
+
+  const int nq = a.q.n_heads, heads = nq + a.k.n_heads;
+  const int groups = (heads + per - 1) / per;
+  const float inv_d = 1.0f / float(d);
+  const T *qi = reinterpret_cast<const T *>(a.q.in) + b * a.q.in_batch + r * a.q.in_row;
+  const T *ki = reinterpret_cast<const T *>(a.k.in) + b * a.k.in_batch + r * a.k.in_row;
+  T *qo = reinterpret_cast<T *>(a.q.out) + b * a.q.out_batch + r * a.q.out_row;
+  T *ko = reinterpret_cast<T *>(a.k.out) + b * a.k.out_batch + r * a.k.out_row;
 
   // kPairs, kHalves: cos and sin of the lane's four pairs; kShared: of its eight elements'
   constexpr int NF = PARTNER == kNone ? 1 : PARTNER == kShared ? 8 : 4;
@@ -107,13 +118,6 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
     }
   }
 
-  const int nq = a.q.n_heads, heads = nq + a.k.n_heads;
-  const int groups = (heads + per - 1) / per;
-  const float inv_d = 1.0f / float(d);
-  const T *qi = reinterpret_cast<const T *>(a.q.in) + b * a.q.in_batch + r * a.q.in_row;
-  const T *ki = reinterpret_cast<const T *>(a.k.in) + b * a.k.in_batch + r * a.k.in_row;
-  T *qo = reinterpret_cast<T *>(a.q.out) + b * a.q.out_batch + r * a.q.out_row;
-  T *ko = reinterpret_cast<T *>(a.k.out) + b * a.k.out_batch + r * a.k.out_row;
   for (int g0 = part * p.chunk; g0 < groups; g0 += p.parts * p.chunk) {
     typename V::R ra[kAhead], rb[kAhead];
 #pragma unroll
@@ -130,67 +134,71 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
     for (int u = 0; u < kAhead; ++u) {
       if (u >= p.chunk || g0 + u >= groups) break;  // the same for the whole warp
       const int hh = (g0 + u) * per + slot;
-      float x[8];
+      // elements two by two: e0, e0 + 1 | .. | e1 + 2, e1 + 3
+      float2 x[4];
       V::get(ra[u], x);
-      V::get(rb[u], x + 4);
+      V::get(rb[u], x + 2);
       if (a.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+        const float2 s2 = ffma2(x[3], x[3], ffma2(x[2], x[2], ffma2(x[1], x[1], fmul2(x[0], x[0]))));
+        float ss = s2.x + s2.y;
         for (int m = lanes >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= inv;
+        for (int j = 0; j < 4; ++j) x[j] = fmul2(x[j], make_float2(inv, inv));
         const float *weight = hh < nq ? a.q.weight : a.k.weight;
         if (weight && live) {
           const float4 w0 = __ldg(reinterpret_cast<const float4 *>(weight + e0));
           const float4 w1 = __ldg(reinterpret_cast<const float4 *>(weight + e1));
-          const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= w[j];
+          x[0] = fmul2(x[0], make_float2(w0.x, w0.y));
+          x[1] = fmul2(x[1], make_float2(w0.z, w0.w));
+          x[2] = fmul2(x[2], make_float2(w1.x, w1.y));
+          x[3] = fmul2(x[3], make_float2(w1.z, w1.w));
         }
       }
-      float y[8];
+      float2 y[4];
       if constexpr (PARTNER == kNone) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j];
-      } else if constexpr (PARTNER == kPairs || PARTNER == kHalves) {
+        for (int j = 0; j < 4; ++j) y[j] = x[j];
+      } else if constexpr (PARTNER == kPairs) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int f = PARTNER == kPairs ? 2 * j : j, s = PARTNER == kPairs ? 2 * j + 1 : j + 4;
-          y[f] = fmaf(x[f], cs[j], -x[s] * sn[j]);
-          y[s] = fmaf(x[s], cs[j], x[f] * sn[j]);
-          if (PARTNER == kPairs && e0 + 2 * j >= rot) {  // not rotated: as it is, whatever its pair holds
-            y[f] = x[f];
-            y[s] = x[s];
-          }
+          y[j] = make_float2(fmaf(x[j].x, cs[j], -x[j].y * sn[j]), fmaf(x[j].y, cs[j], x[j].x * sn[j]));
+          if (e0 + 2 * j >= rot) y[j] = x[j];  // not rotated: as it is, whatever its pair holds
+        }
+      } else if constexpr (PARTNER == kHalves) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 c2 = make_float2(cs[2 * j], cs[2 * j + 1]), s2 = make_float2(sn[2 * j], sn[2 * j + 1]);
+          const float2 n2 = make_float2(-s2.x, -s2.y);
+          y[j] = ffma2(x[j], c2, fmul2(x[j + 2], n2));
+          y[j + 2] = ffma2(x[j + 2], c2, fmul2(x[j], s2));
         }
       } else {
         // each lane's eight elements at 8 lane: the warp's heads side by side
         float *st = s_stage + warp * 256;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) st[8 * lane + j] = x[j];
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<float2 *>(&st[8 * lane + 2 * j]) = x[j];
         __syncwarp();
+        auto turn = [&](float v, int j) {
+          const int e = e0 + j, other = e < half ? e + half : e - half;
+          return e < rot ? fmaf(v, cs[j], st[8 * (lane - li) + other] * sn[j]) : v;
+        };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          const int other = e < half ? e + half : e - half;
-          y[j] = e < rot ? fmaf(x[j], cs[j], st[8 * (lane - li) + other] * sn[j]) : x[j];
-        }
+        for (int j = 0; j < 4; ++j) y[j] = make_float2(turn(x[j].x, 2 * j), turn(x[j].y, 2 * j + 1));
       }
       if (live && hh < heads) {
         T *dst = hh < nq ? qo + hh * a.q.out_head : ko + (hh - nq) * a.k.out_head;
         *reinterpret_cast<typename V::R *>(dst + e0) = V::put(y);
-        *reinterpret_cast<typename V::R *>(dst + e1) = V::put(y + 4);
+        *reinterpret_cast<typename V::R *>(dst + e1) = V::put(y + 2);
       }
     }
   }
 }
 
 template <typename T>
-void heads_launch(const HeadsParams &p, int partner, unsigned grid, cudaStream_t s) {
-  const dim3 g(grid), blk(32 * kHeadWarps);
+void heads_launch(const HeadsParams &p, int partner, dim3 g, cudaStream_t s) {
+  const dim3 blk(32 * kHeadWarps);
   if (partner == kNone) launch_kernel(qk_norm_rope_kernel<T, kNone>, g, blk, 0, s, p);
   else if (partner == kPairs) launch_kernel(qk_norm_rope_kernel<T, kPairs>, g, blk, 0, s, p);
   else if (partner == kHalves) launch_kernel(qk_norm_rope_kernel<T, kHalves>, g, blk, 0, s, p);
@@ -223,7 +231,8 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
                       : a.rope.dim == a.head_dim ? kHalves : kShared;
   // One warp per row amortises the row's angles over all of its heads; with too few rows to
   // give every SM 16 warps, a row's heads are split over several warps, down to one load of
-  // 32 / lanes heads each.
+  // 32 / lanes heads each.  (A warp over the same row of several sequences, which could share
+  // the angles, was slower: 73 against 64 us at 8 x 4224 rows of 30 heads.)
   const int heads = a.q.n_heads + a.k.n_heads, per = 32 / p.lanes;
   const long long rows = (long long)a.batch * a.n_rows;
   const int loads = (heads + per - 1) / per;
@@ -231,14 +240,15 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
   p.parts = int(want < loads ? want : loads);
   p.chunk = (loads + p.parts - 1) / p.parts;
   if (p.chunk > kAhead) p.chunk = kAhead;
-  p.units = rows * p.parts;
-  const long long grid = (p.units + kHeadWarps - 1) / kHeadWarps;
-  if (grid > 0x7fffffffLL) {
+  const long long units = rows * p.parts;
+  if (units > 0x7fffffffLL) {
     set_error("too many rows");
     return HYMBA_ERR_UNSUPPORTED;
   }
-  if (a.dtype == HYMBA_BF16) heads_launch<__nv_bfloat16>(p, partner, (unsigned)grid, s);
-  else heads_launch<float>(p, partner, (unsigned)grid, s);
+  p.units = (unsigned)units;
+  const dim3 grid((unsigned)((units + kHeadWarps - 1) / kHeadWarps));
+  if (a.dtype == HYMBA_BF16) heads_launch<__nv_bfloat16>(p, partner, grid, s);
+  else heads_launch<float>(p, partner, grid, s);
   note_launch(1);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

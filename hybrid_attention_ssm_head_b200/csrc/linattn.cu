@@ -13,8 +13,8 @@ namespace {
 // ---------------------------------------------------------------------------
 // one token per sequence
 // ---------------------------------------------------------------------------
-constexpr int kStepWarps = 8;
-constexpr int kStepAhead = 8;  // 16-byte state loads in flight per lane
+constexpr int kStepWarps = 4;
+constexpr int kStepAhead = 4;  // 16-byte state loads in flight per lane
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p) {
@@ -28,12 +28,16 @@ __device__ __forceinline__ float4 load4(const T *p) {
 
 // Bound by the state's bytes, read and written once.  A CTA takes `rows` of the dv state
 // rows of one (sequence, head); LANES lanes hold one row, four columns each, so a warp's loads
-// and stores are whole contiguous rows.  A lane's eight rows are requested together.  Their
-// dot products with q are summed over the lanes by halves: each exchange hands half of the
-// rows' sums to the other half of the lanes, so eight sums over LANES >= 8 lanes take 7 +
-// log2(LANES / 8) shuffles and each lands in a lane of its own, which finishes that row.
+// and stores are whole contiguous rows.  A lane's rows are requested together.  Their dot
+// products with q are summed over the lanes by halves: each exchange hands half of the rows'
+// sums to the other half of the lanes, so four sums over LANES >= 4 lanes take 3 +
+// log2(LANES / 4) shuffles and each lands in a lane of its own, which finishes that row.
+// Many small CTAs cover each other's ends: with 8 warps and 8 rows a lane, 4 CTAs to an SM,
+// 128 x 25 heads of 128 x 64 states took 50 us, with 4 warps and 4 rows, 12 to an SM, 41 us, and
+// with the state marked as read and written once (it is back only when every other layer's
+// has passed through the cache) 39 us, 5.4 TB/s.
 template <typename T, int LANES>
-__global__ void __launch_bounds__(32 * kStepWarps, 4)
+__global__ void __launch_bounds__(32 * kStepWarps, 12)
     linear_step_kernel(const __grid_constant__ hymba_linear_attention a, int rows) {
   pdl_wait();
   pdl_trigger();
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, 4)
     k = load4(reinterpret_cast<const T *>(a.k) + b * a.k_batch + hk * a.k_head + c0);
     q = load4(reinterpret_cast<const T *>(a.q) + b * a.q_batch + hk * a.q_head + c0);
   }
-  // which of its eight rows' sums a lane ends up with, from its number's high bits down; of
+  // which of its rows' sums a lane ends up with, from its number's high bits down; of
   // the lanes that share one the first finishes it
   int u0 = 0;
 #pragma unroll
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, 4)
       st[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       v[u] = 0.f;
       if (p < p_end) {
-        if (live && sin) st[u] = *reinterpret_cast<const float4 *>(sin + (long long)p * a.dk + c0);
+        if (live && sin) st[u] = __ldcs(reinterpret_cast<const float4 *>(sin + (long long)p * a.dk + c0));
         v[u] = Store<T>::to_f(vp[p]);
       }
     }
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, 4)
         st[u].w = fmaf(decay, st[u].w, x * k.w);
       }
       dot[u] = fmaf(st[u].x, q.x, st[u].y * q.y) + fmaf(st[u].z, q.z, st[u].w * q.w);
-      if (live && p < p_end) *reinterpret_cast<float4 *>(sout + (long long)p * a.dk + c0) = st[u];
+      if (live && p < p_end) __stcs(reinterpret_cast<float4 *>(sout + (long long)p * a.dk + c0), st[u]);
     }
     int n = kStepAhead / 2;
 #pragma unroll
@@ -336,7 +340,8 @@ void scan_launch(const hymba_linear_attention &a, LinearSegments g, cudaStream_t
   }
 }
 
-// Few heads of many rows: segments of at least 32 rows, about eight CTAs for each SM.
+// Few heads of many rows: segments of at least 32 rows, about eight CTAs for each SM (2 x 4 heads
+// of 1031 fp32 rows: 433 us whole, 82 us so).
 LinearSegments scan_segments(const hymba_linear_attention &a) {
   LinearSegments g{};
   const long long ctas = (long long)a.batch * a.n_heads * ((a.dv + kScanState - 1) / kScanState);
@@ -364,9 +369,9 @@ size_t segment_state_bytes(const hymba_linear_attention &a, const LinearSegments
 hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s) {
   int lanes = 2;
   while (lanes * 4 < a.dk) lanes *= 2;
-  // One CTA for all state rows of a (sequence, head) keeps eight loads in flight per lane;
-  // with fewer (sequence, head) pairs than two CTAs for each SM the rows are split, down to
-  // one load per lane.
+  // One CTA for all state rows of a (sequence, head) keeps four loads in flight per lane; with
+  // fewer (sequence, head) pairs than two CTAs for each SM the rows are split, down to one
+  // load per lane.
   const int once = kStepWarps * (32 / lanes);
   const int most = (a.dv + once - 1) / once;
   const long long pairs = (long long)a.batch * a.n_heads;

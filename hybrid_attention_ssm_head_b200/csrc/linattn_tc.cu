@@ -447,8 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = len - c * C - 32 * w;  // rows of this warp that count (may be none)
       if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
       const float e = dec[c & 1].e[r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
       if (Lay::GATE && gates && !warp_wait(z_full, ph, wlim)) break;
       const uint8_t *vs = smem + st * Lay::STAGE + Lay::V + row;
       if (!warp_wait(o_full, ph, wlim)) break;
@@ -467,10 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane < rows && 8 * (x0 + x) < pn - first) z[x] = __ldg(reinterpret_cast<const uint4 *>(zrow + 16 * (x0 + x)));
             }
           }
-        }
-        if (x0 + 4 == 4 * NV) {  // the gate's tile has been read: the next one can come
-          __syncwarp();
-          if (lane == 0) mbar_arrive(z_empty);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {  // 8 columns: one piece of v, the gate and o
@@ -505,9 +499,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
+      // Only here, behind the use of what was read: an arrival does not wait for loads that are
+      // still on their way, and a tile released before them was overwritten under them.
       if (lane == 0) {
         mbar_arrive(o_empty);
-        mbar_arrive(&empty[st]);  // V has been read
+        mbar_arrive(&empty[st]);  // V
+        mbar_arrive(z_empty);
+        mbar_arrive(&dec_empty[c & 1]);
       }
       if (gates) zrow += 2 * C * a.gate_row;
       orow += 2 * C * a.o_row;
@@ -527,8 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           !warp_wait(c_full, ph ^ 1u, wlim) || (outputs && !warp_wait(qs_done, ph, wlim)))
         break;
       const float wj = dec[c & 1].w[r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
       uint8_t *krow = smem + st * Lay::STAGE + Lay::K + r * 128, *mrow = smem + Lay::MID + r * 128;
       uint8_t *qrow = smem + st * Lay::STAGE + Lay::Q + r * 128;
       const float2 w2 = make_float2(wj, wj);
@@ -560,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async();
       mbar_arrive(k_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<NK>::STATE));
@@ -627,8 +625,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(sb_full);
       if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) { ok = false; break; }
       const float decay = dec[c & 1].end;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
       if (!warp_wait(c_full, ph, wlim)) { ok = false; break; }
       tc_fence_after();
       const float2 d2 = make_float2(decay, decay);
@@ -649,7 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(c_empty);
+      if (lane == 0) {
+        mbar_arrive(c_empty);
+        mbar_arrive(&dec_empty[c & 1]);
+      }
     }
     float *dst = !outputs ? prm.seg.state + (long long)bhs * dense
                  : a.state_out && seg == prm.seg.n - 1 ? a.state_out + (long long)bh * dense : nullptr;
