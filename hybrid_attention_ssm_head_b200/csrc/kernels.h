@@ -320,17 +320,24 @@ struct LinearInputsArgs {
   int N, H;
 };
 hymba_status linear_inputs(const LinearInputsArgs &a, hymba_dtype dt, cudaStream_t s);
-// The rows of few heads split into segments: pass 0 computes each segment's own state (from
-// zero, the first from the call's) and the sum of its log decays, all but the last one's;
-// pass 1 the outputs, each segment from the states before it.  n = 1: pass 1 alone.
+// The rows split into n segments of `rows` rows (n = 1: whole).
+// Few heads: pass 0 computes each segment's own state (from zero, the first from the call's)
+// and the sum of its log decays, all but the last one's; pass 1 the outputs, each segment from
+// the states before it.
+// Many heads (chain): pass 1 alone, each segment from the state that the one before it leaves.
 struct LinearSegments {
-  int n, rows;    // segments of `rows` rows
+  int n, rows;
+  int chain;
   int pass;
-  float *state;   // [n, batch * n_heads, dv, dk]; the last slot holds a copy of the call's state
-  double *decay;  // [n, batch * n_heads] log2 of the segments' decays
+  float *state;      // [n, batch * n_heads, dv, dk]; the last slot holds a copy of the call's
+                     // state.  chain: [batch * n_heads, dv, dk], the state between segments
+  double *decay;     // [n, batch * n_heads] log2 of the segments' decays
+  unsigned *ticket;  // chain: [1 + batch * n_heads * dv blocks] zeroed: the next segment to
+                     // take, and how many warps have left each chain's state
 };
 // ... of bf16 storage on the tensor cores.
 LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a);
+size_t linear_attention_tc_tickets(const hymba_linear_attention &a);  // words of a chain's tickets
 hymba_status linear_attention_tc(const hymba_linear_attention &a, const LinearSegments &seg, cudaStream_t s);
 size_t linear_attention_workspace_bytes(const hymba_linear_attention &a);
 // A rotation's own numbers, for heads of `width` elements.

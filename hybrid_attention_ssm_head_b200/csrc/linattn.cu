@@ -360,8 +360,12 @@ bool on_tensor_cores(const hymba_linear_attention &a) { return a.dtype == HYMBA_
 LinearSegments segments_of(const hymba_linear_attention &a) {
   return on_tensor_cores(a) ? linear_attention_tc_segments(a) : scan_segments(a);
 }
+// The workspace of a split: states, then the segments' decays or the chain's tickets.
 size_t segment_state_bytes(const hymba_linear_attention &a, const LinearSegments &g) {
-  return (size_t)g.n * a.batch * a.n_heads * a.dv * a.dk * 4;
+  return (size_t)(g.chain ? 1 : g.n) * a.batch * a.n_heads * a.dv * a.dk * 4;
+}
+size_t segment_rest_bytes(const hymba_linear_attention &a, const LinearSegments &g) {
+  return g.chain ? linear_attention_tc_tickets(a) * 4 : (size_t)g.n * a.batch * a.n_heads * 8;
 }
 
 }  // namespace
@@ -393,7 +397,7 @@ hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t
 
 size_t linear_attention_workspace_bytes(const hymba_linear_attention &a) {
   const LinearSegments g = segments_of(a);
-  return g.n > 1 ? segment_state_bytes(a, g) + (size_t)g.n * a.batch * a.n_heads * 8 : 0;
+  return g.n > 1 ? (segment_state_bytes(a, g) + segment_rest_bytes(a, g) + 7) / 8 * 8 : 0;
 }
 
 hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, cudaStream_t s, int whole_batch) {
@@ -402,7 +406,13 @@ hymba_status linear_attention(const hymba_linear_attention &a, void *workspace, 
   LinearSegments g = segments_of(whole);
   if (g.n > 1) {
     g.state = reinterpret_cast<float *>(workspace);
-    g.decay = reinterpret_cast<double *>(reinterpret_cast<char *>(workspace) + segment_state_bytes(whole, g));
+    char *rest = reinterpret_cast<char *>(workspace) + segment_state_bytes(whole, g);
+    g.decay = reinterpret_cast<double *>(rest);
+    g.ticket = reinterpret_cast<unsigned *>(rest);
+    if (g.chain && cudaMemsetAsync(rest, 0, segment_rest_bytes(a, g), s) != cudaSuccess) {
+      set_error("cudaMemsetAsync(segment tickets): %s", cudaGetErrorString(cudaGetLastError()));
+      return HYMBA_ERR_CUDA;
+    }
   }
   if (on_tensor_cores(a)) return linear_attention_tc(a, g, s);
   if (a.dtype == HYMBA_BF16) scan_launch<__nv_bfloat16>(a, g, s);

@@ -83,6 +83,11 @@ __device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, unsigne
     }
   return true;
 }
+__device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 // ... by a whole warp: all of its lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned limit) {
   return __all_sync(0xffffffffu, one_wait(bar, parity, limit));
@@ -123,8 +128,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const hymba_linear_attention &a = prm.a;
   const int warp = warp_id(), lane = lane_id();
   const unsigned wlim = prm.wlim;
-  const int blk = blockIdx.x % prm.blocks;
-  const int bhs = blockIdx.x / prm.blocks;
+  // A chain's segments are handed out in order, first the first of every chain: a CTA waits
+  // only for a segment that a CTA has taken before it, so every wait ends.
+  unsigned task = blockIdx.x;
+  if (prm.seg.chain) {
+    if (threadIdx.x == 0) tmem_slot[2] = atomicAdd(prm.seg.ticket, 1u);
+    __syncthreads();
+    task = tmem_slot[2];
+  }
+  const int blk = task % prm.blocks;
+  const int bhs = task / prm.blocks;
   const int bh = bhs % (a.batch * a.n_heads), seg = bhs / (a.batch * a.n_heads);
   const int h = bh % a.n_heads, b = bh / a.n_heads;
   const int hk = h / (a.n_heads / a.n_qk_heads);
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int n = 0; n < 64 * NK; n += 4)
         if (mine && n < a.dk) {
-          const float4 x = *reinterpret_cast<const float4 *>(src + at + n);
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + at + n));  // other SMs' stores among them
           S[n / 2] = ffma2(make_float2(keep, keep), S[n / 2], make_float2(x.x, x.y));
           S[n / 2 + 1] = ffma2(make_float2(keep, keep), S[n / 2 + 1], make_float2(x.z, x.w));
         }
@@ -584,11 +597,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // own states, each decayed by those after it.
     const long long heads = (long long)a.batch * a.n_heads;
     const float *from = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
-    if (outputs && prm.seg.n > 1) from = a.state_in ? prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense : nullptr;
-    const int first = outputs ? 0 : seg;  // a segment's own state starts from zero
+    if (outputs && prm.seg.n > 1 && !prm.seg.chain)
+      from = a.state_in ? prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense : nullptr;
+    const int first = outputs && !prm.seg.chain ? 0 : seg;  // a segment's own state starts from zero
+    unsigned *left = prm.seg.ticket + 1 + bh * prm.blocks + blk;  // chain: four warps for each segment
+    bool ok = !failed;
+    if (prm.seg.chain && seg > 0) {
+      if (ok && lane == 0) {
+        const unsigned t0 = (unsigned)clock();
+        while (load_acquire(left) < 4u * seg)
+          if ((unsigned)clock() - t0 > wlim) {
+            atomicOr(&g_err_lin, kErrTimeout);
+            ok = false;
+            break;
+          }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      from = prm.seg.state + bh * dense;
+    }
+#pragma unroll 1
     for (int j = first; j <= seg; ++j) {
-      const float *src = j > first ? prm.seg.state + ((j - 1) * heads + bh) * dense : seg == 0 ? from : nullptr;
-      if (src) add_row(src, j > first ? exp2f((float)prm.seg.decay[(j - 1) * heads + bh]) : 0.f);
+      const bool start = j == first;
+      const float *src = !start ? prm.seg.state + ((j - 1) * heads + bh) * dense : seg == 0 || prm.seg.chain ? from : nullptr;
+      if (ok && src) add_row(src, start ? 0.f : exp2f((float)prm.seg.decay[(j - 1) * heads + bh]));
     }
     auto store_state = [&](float *dst) {
 #pragma unroll
@@ -598,8 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!outputs && seg == 0 && a.state_in)  // a copy for the outputs' pass, which may write in place
       store_state(prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense);
-    bool ok = !failed;
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; ok && c < chunks; ++c) {
       const uint32_t ph = uint32_t(c) & 1u;
       // the state as the operand of Q S^T: high and low bf16 parts.  The buffer's last reader,
       // the chunk before's Q S^T, is behind its P V or its state product.
@@ -652,7 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     float *dst = !outputs ? prm.seg.state + (long long)bhs * dense
                  : a.state_out && seg == prm.seg.n - 1 ? a.state_out + (long long)bh * dense : nullptr;
+    const bool hand_on = prm.seg.chain && seg < prm.seg.n - 1;
+    if (hand_on) dst = prm.seg.state + bh * dense;
     if (ok && dst) store_state(dst);
+    if (ok && hand_on) {
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) atomicAdd(left, 1u);
+    }
   }
 
   tc_fence_before();
@@ -712,7 +749,7 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
     set_error("too many sequences and heads");
     return HYMBA_ERR_UNSUPPORTED;
   }
-  for (p.seg.pass = seg.n > 1 ? 0 : 1; p.seg.pass < 2; ++p.seg.pass) {
+  for (p.seg.pass = seg.n > 1 && !seg.chain ? 0 : 1; p.seg.pass < 2; ++p.seg.pass) {
     const long long grid = ctas * (p.seg.pass ? seg.n : seg.n - 1);
     launch_kernel(linear_chunk_kernel<NK, NV>, dim3((unsigned)grid), dim3(kThreads), (size_t)Lay::TOTAL, s, tq, tk, tv, tz, p);
     note_launch(1);
@@ -733,16 +770,42 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
 // the time in n segments, and a second launch about as long as four chunks: 25 heads of 8320
 // rows 450 us whole and 163 us in five segments, 28 heads of 517 rows 18 us whole and 28 us
 // in two.
+//
+// More heads than SMs run in rounds, the last of which leaves SMs idle.  Then each head's rows
+// are a chain of segments that CTAs take up in turn, so that the rounds are shorter; a CTA's
+// start and end cost about as much as 0.7 of a chunk: 200 heads of 4224 rows 288 us whole and
+// 237 us in chains of two.
 LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a) {
   LinearSegments g{};
   const long long ctas = (long long)a.batch * a.n_heads * dv_blocks(a);
   const int chunks = (a.n_rows + C - 1) / C;
-  const long long most = std::max<long long>(1, std::min<long long>(148 / std::max<long long>(1, ctas), chunks / 2));
-  const int per = (chunks + (int)most - 1) / (int)most, n = (chunks + per - 1) / per;
-  const bool split = 5 * chunks * (long long)n - 8 * chunks >= 20 * (long long)n;  // chunks (1 - 1.6 / n) >= 4
-  g.n = split ? n : 1;
-  g.rows = (split ? per : chunks) * C;
+  g.n = 1;
+  g.rows = chunks * C;
+  if (ctas <= 148) {
+    const long long most = std::max<long long>(1, std::min<long long>(148 / std::max<long long>(1, ctas), chunks / 2));
+    const int per = (chunks + (int)most - 1) / (int)most, n = (chunks + per - 1) / per;
+    if (5 * chunks * (long long)n - 8 * chunks >= 20 * (long long)n) {  // chunks (1 - 1.6 / n) >= 4
+      g.n = n;
+      g.rows = per * C;
+    }
+    return g;
+  }
+  double best = 0.0;
+  for (int per = chunks; per >= 4; --per) {  // segments of at least four chunks
+    const int n = (chunks + per - 1) / per;
+    const double cost = (double)((ctas * n + 147) / 148) * (per + 0.7);
+    if (per == chunks || cost < 0.97 * best) {
+      best = cost;
+      g.n = n;
+      g.rows = per * C;
+    }
+  }
+  g.chain = g.n > 1;
   return g;
+}
+
+size_t linear_attention_tc_tickets(const hymba_linear_attention &a) {
+  return 1 + (size_t)a.batch * a.n_heads * dv_blocks(a);
 }
 
 hymba_status linear_attention_tc(const hymba_linear_attention &a, const LinearSegments &seg, cudaStream_t s) {

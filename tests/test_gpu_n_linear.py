@@ -85,6 +85,8 @@ CASES = [
     ("bf16", 2, 1000, 2, 1, 64, 128, "token", True, True, None),
     ("bf16", 3, 900, 2, 2, 128, 72, "head", True, True, [0, 130, 900]),
     ("bf16", 1, 1290, 1, 1, 16, 200, "strong", False, False, None),
+    # more heads than SMs: chains of segments
+    ("bf16", 30, 1030, 5, 1, 32, 64, "token", True, True, [0, 1, 128, 513, 1029] + [1030] * 25),
     # few rows: one after another
     ("bf16", 2, 9, 3, 1, 72, 40, "token", True, True, [9, 4]),
     ("f32", 2, 1, 4, 1, 64, 128, "token", True, True, None),
