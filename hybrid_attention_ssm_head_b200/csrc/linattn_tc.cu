@@ -30,8 +30,8 @@ constexpr int kThreads = 768;
 // thread.
 template <int NK>
 struct Regs {
-  static constexpr int LAUNCH = 80, CTRL = NK == 1 ? 72 : 64, SCORES = NK == 1 ? 80 : 72, KEYS = 56;
-  static constexpr int OUT = NK == 1 ? 80 : 64, STATE = NK == 1 ? 112 : 160;
+  static constexpr int LAUNCH = 80, CTRL = 64, SCORES = NK == 1 ? 72 : 64, KEYS = 80;
+  static constexpr int OUT = NK == 1 ? 72 : 56, STATE = NK == 1 ? 120 : 160;
   static_assert(CTRL + SCORES + KEYS + 2 * OUT + STATE == 6 * LAUNCH, "the warpgroups share the launch's registers");
 };
 constexpr int kAtom = C * 128;  // bytes of 128 rows x 64 bf16 columns, 128-byte swizzle
@@ -58,8 +58,7 @@ struct Layout {
   static constexpr int SB_PART = NK * NV * (kAtom / 2); // 64 NV rows of 128 bytes per dk atom
   // the state product reads 128 state rows whatever dv is: for NV = 1 up to one atom behind V
   static constexpr int Z = SB + 2 * SB_PART;            // gate tile
-  static constexpr int OUT = Z + (GATE ? NV * kAtom : 0);  // output: 32 rows of 32 bytes per warp
-  static constexpr int DEC = OUT + 8 * 1024;
+  static constexpr int DEC = Z + (GATE ? NV * kAtom : 0);
   static constexpr int SKIP = DEC + 2 * (int)sizeof(Decays);
   static constexpr int BAR = SKIP + NV * 64 * 4;
   static constexpr int TOTAL = BAR + 32 * 8 + 1024;  // + alignment of the base
@@ -71,26 +70,24 @@ __device__ __forceinline__ uint32_t high_pair(float2 x) {
   return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
 }
 
-// A bounded wait as in common.cuh, in few instructions: the roles' loops have to stay in the
-// instruction cache together (see the kernel).  A CTA that starts after another has given up
-// does nothing.
+// A bounded wait as in common.cuh, in few instructions, since the roles share an instruction
+// cache (see the kernel).  A role that gives up leaves its loop early,
+// which the end of the kernel reports; a CTA that starts after that does nothing.
 __device__ __forceinline__ bool one_wait(uint64_t *bar, uint32_t parity, unsigned limit) {
   const unsigned t0 = (unsigned)clock();
   while (!mbar_try_wait(bar, parity))
-    if ((unsigned)clock() - t0 > limit) {
-      atomicOr(&g_err_lin, kErrTimeout);
-      return false;
-    }
+    if ((unsigned)clock() - t0 > limit) return false;
   return true;
-}
-__device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
-  unsigned v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
 }
 // ... by a whole warp: all of its lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned limit) {
   return __all_sync(0xffffffffu, one_wait(bar, parity, limit));
+}
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
 struct Params {
@@ -100,6 +97,35 @@ struct Params {
   unsigned wlim;   // bounded waits: SM clock cycles
 };
 
+// One CTA takes one head's (or segment's) chunks.  A chunk c runs through warps of different
+// roles, each a chunk or so ahead of the next one:
+//   TMA      Q, K, V, gate tiles of c + 1, c + 2
+//   decays   sums of the log decays by an fp64 scan, and the factors that come from them
+//   MMA      Q K^T(c + 1) | Q S^T(c) | V^T K'(c) | P V(c) onto the scaled Q S^T, in this order
+//   scores   P over Q K^T in tensor memory, as the operand of P V
+//   keys     the three parts of the weighted keys, ready but for the low ones' stores before
+//            Q S^T is through with the queries
+//   output   exp(G) Q S^T + skip v in place (of c + 1), then gate and store (of c): two
+//            accumulators, so that the loop through the state does not wait for an output
+//   state    fp32 state in registers: decayed, the chunk's sum added, split for Q S^T
+// What has to follow one another, chunk by chunk, is state operand -> Q S^T -> low parts ->
+// V^T K' -> state: about 6300 cycles a chunk, of which the products are 1300; the rest are the
+// roles' CUDA-core instructions and the waits between them.  Six warps share a scheduler that
+// issues in 43 % of the cycles, stalled on shared memory (which the operands of the products
+// and the tiles take for half of the time) and on each other; shortening the chain alone, by
+// buffers of its own for the low parts, made nothing faster.  HBM is at half of its rate: 400
+// heads of 8320 rows, dk 64, dv 128, 745 us for 401 us of bytes.
+//   measured, 200 heads of 4224 rows / 25 of 8320 rows with dk 128 / 400 of 8320 rows:
+//     one output accumulator, 32 columns at a time                   237 / 170 / 842 us
+//     16 columns at a time (less code, fewer registers)              227 / 165 / 792 us
+//     scores 16 columns at a time, errors reported in one place      225 / 162 / 790 us
+//     keys ahead of Q S^T, V released of its own                     227 / 147 / 788 us
+//     two output accumulators, skip v ahead, rows stored directly    214 / 153 / 743 us
+//     gate by cp.async in place of TMA, to free a buffer for the
+//     low parts                                                      269 / 158 / 967 us
+//     the tiles brought into L2 ahead                                222 / 150 / 765 us
+// The code of all roles together matters: 8 % between two builds of the same work when one
+// was 5 KB above the other's 71 KB.
 template <int NK, int NV>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -112,16 +138,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::BAR);
-  uint64_t *full = bars + 0, *empty = bars + 2;            // [ST] Q, K, V stages
-  uint64_t *dec_full = bars + 4, *dec_empty = bars + 6;    // [2] decays
-  uint64_t *s_full = bars + 10, *p_full = bars + 11;       // scores ready / P written over them
-  uint64_t *o_full = bars + 12, *o_empty = bars + 13;      // outputs ready / read
-  uint64_t *z_full = bars + 8, *z_empty = bars + 9;        // gate tile
-  uint64_t *k_full = bars + 15;                            // weighted keys ready
-  uint64_t *c_full = bars + 18, *c_empty = bars + 19;      // the chunk's state ready / read
-  uint64_t *sb_full = bars + 20, *qs_done = bars + 21;     // state operand ready / Q S^T done
-  uint64_t *drain = bars + 22;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23);
+  // [2] each: a stage's (Q, K) and V tiles, decays, scores, outputs.  A barrier of which a
+  // warp may look at one phase when the next is over already has two, by the chunk's parity.
+  uint64_t *full = bars + 0, *empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 6;
+  uint64_t *dec_full = bars + 8, *dec_empty = bars + 10;
+  uint64_t *s_full = bars + 12;                          // scores ready
+  uint64_t *o_full = bars + 14, *o_empty = bars + 16;    // outputs ready / read
+  uint64_t *z_full = bars + 18, *z_empty = bars + 19;    // gate tile
+  uint64_t *p_full = bars + 20, *x_full = bars + 21;     // P written over the scores / Q S^T scaled
+  uint64_t *k_full = bars + 22;                          // weighted keys ready
+  uint64_t *c_full = bars + 23, *c_empty = bars + 24;    // the chunk's state ready / read
+  uint64_t *sb_full = bars + 25, *qs_done = bars + 26;   // state operand ready / Q S^T done
+  uint64_t *drain = bars + 27;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 28);
   Decays *dec = reinterpret_cast<Decays *>(smem + Lay::DEC);
   float *s_skip = reinterpret_cast<float *>(smem + Lay::SKIP);
 
@@ -151,16 +180,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&full[x], 1);
-      mbar_init(&empty[x], outputs ? 1 + 8 : 1);  // products retired, V read by the output's warps
+      mbar_init(&empty[x], 1);
+      mbar_init(&v_full[x], 1);
+      mbar_init(&v_empty[x], outputs ? 1 + 8 : 1);  // products retired, V read by the output's warps
       mbar_init(&dec_full[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&o_empty[x], 8);
       mbar_init(&dec_empty[x], outputs ? 20 : 8);
     }
-    mbar_init(s_full, 1);
     mbar_init(z_full, 1);
     mbar_init(z_empty, 8);
     mbar_init(p_full, 4);
-    mbar_init(o_full, 1);
-    mbar_init(o_empty, 8);
+    mbar_init(x_full, 8);
     mbar_init(k_full, 128);
     mbar_init(c_full, 1);
     mbar_init(c_empty, 4);
@@ -185,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot[0];
   const bool failed = tmem_slot[1] != 0u;
   const int chunks = failed ? 0 : (len + C - 1) / C;
-  const uint32_t tS = tmem, tO = tmem + 128, tX = tmem + 256, tC = tmem + 384;
+  const uint32_t tS = tmem, tO = tmem + 128, tC = tmem + 384;  // tO: two chunks' outputs
+  bool gave_up = false;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::CTRL));
@@ -199,17 +232,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ph = uint32_t(c / ST) & 1u;
           if (!one_wait(&empty[st], ph ^ 1u, wlim)) { ok = false; break; }
           uint8_t *dst = smem + st * Lay::STAGE;
-          mbar_arrive_expect_tx(&full[st], outputs ? Lay::STAGE : Lay::STAGE - NK * kAtom);
+          mbar_arrive_expect_tx(&full[st], (outputs ? 2 : 1) * NK * kAtom);
           for (int x = 0; x < NK; ++x) {
             tma_load_4d(dst + Lay::K + x * kAtom, &tmK, &full[st], 64 * x, hk, base + c * C, b);
             if (outputs) tma_load_4d(dst + Lay::Q + x * kAtom, &tmQ, &full[st], 64 * x, hk, base + c * C, b);
           }
+          if (!one_wait(&v_empty[st], ph ^ 1u, wlim)) { ok = false; one_wait(&full[st], ph, wlim); break; }
+          mbar_arrive_expect_tx(&v_full[st], NV * kAtom);
           for (int x = 0; x < NV; ++x)
-            tma_load_4d(dst + Lay::V + x * kAtom, &tmV, &full[st], p0 + 64 * x, h, base + c * C, b);
+            tma_load_4d(dst + Lay::V + x * kAtom, &tmV, &v_full[st], p0 + 64 * x, h, base + c * C, b);
         }
         if (!ok)  // the copies in flight land before the CTA ends
-          for (int q = c > ST ? c - ST : 0; q < c; ++q)
+          for (int q = c > ST ? c - ST : 0; q < c; ++q) {
             one_wait(&full[q % ST], uint32_t(q / ST) & 1u, wlim);
+            one_wait(&v_full[q % ST], uint32_t(q / ST) & 1u, wlim);
+          }
+        gave_up = !ok;
       }
     } else if (warp == 1) {
       if (lane == 0) {
@@ -235,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 4 * NK; ++x)
             if (x < ksteps) mma_bf16_ss(tS, dq + cols(x, kAtom), dk + cols(x, kAtom), idS, x > 0);
-          mma_commit(s_full);
+          mma_commit(&s_full[c & 1]);
           return true;
         };
         bool ok = chunks == 0 || !outputs || scores(0);
@@ -244,9 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ph = uint32_t(c) & 1u;
           const uint32_t q = stage(c, Lay::Q), k = stage(c, Lay::K);
           const uint64_t dv = make_sdesc(stage(c, Lay::V), kAtom, 1024);
+          const uint32_t out = tO + 128 * (c & 1);
           if (outputs) {
             // Q S^T: high part, then low part
-            if (!one_wait(sb_full, ph, wlim) || !one_wait(o_empty, ph ^ 1u, wlim)) break;
+            if (!one_wait(&o_empty[c & 1], (uint32_t(c >> 1) & 1u) ^ 1u, wlim) || !one_wait(sb_full, ph, wlim)) break;
             tc_fence_after();
             const uint64_t dq = make_sdesc(q, 16, 1024), ds = make_sdesc(sb, 16, 1024);
 #pragma unroll
@@ -254,23 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int x = 0; x < 4 * NK; ++x)
                 if (x < ksteps)
-                  mma_bf16_ss(tX, dq + cols(x, kAtom), ds + cols(x, NV * kAtom / 2) + part * (Lay::SB_PART >> 4), idQS,
+                  mma_bf16_ss(out, dq + cols(x, kAtom), ds + cols(x, NV * kAtom / 2) + part * (Lay::SB_PART >> 4), idQS,
                               part > 0 || x > 0);
             mma_commit(qs_done);
-            // in a chunk that ends early P V waits until the rows behind the sequence are zero
-            if (a.lengths && len - c * C < C && !one_wait(k_full, ph, wlim)) break;
-            if (!one_wait(p_full, ph, wlim)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) mma_bf16_ts(tO, tS + 8 * x, dv + x * kRows16, idPV, x > 0);
-            mma_commit(o_full);
-            // the next chunk's scores, ahead of this one's state, where it has a stage
-            if (ST > 1 && c + 1 < chunks && !scores(c + 1)) break;
           }
           // V^T K': high parts (over the keys), middle parts, low parts (over the queries); with
           // dk <= 64 the first two at once, as 64 columns each of one operand, and the low parts
           // added to the middle ones
-          if (!one_wait(k_full, ph, wlim) || !one_wait(c_empty, ph ^ 1u, wlim)) break;
+          if (!one_wait(c_empty, ph ^ 1u, wlim) || !one_wait(&v_full[c % ST], uint32_t(c / ST) & 1u, wlim) ||
+              !one_wait(k_full, ph, wlim))
+            break;
           tc_fence_after();
           auto state_part = [&](uint64_t dk, uint32_t d, uint32_t id, bool add) {
 #pragma unroll
@@ -286,12 +318,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(c_full);
           mma_commit(&empty[c % ST]);
-          if (ST == 1 && outputs && c + 1 < chunks && !scores(c + 1)) break;
+          if (outputs) {
+            // P V onto the scaled Q S^T
+            if (!one_wait(p_full, ph, wlim) || !one_wait(x_full, ph, wlim)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma_bf16_ts(out, tS + 8 * x, dv + x * kRows16, idPV, true);
+            mma_commit(&o_full[c & 1]);
+          }
+          mma_commit(&v_empty[c % ST]);
+          if (outputs && c + 1 < chunks && !scores(c + 1)) break;
           ok = true;
         }
         // the products in flight end before tensor memory is released
         mma_commit(drain);
-        one_wait(drain, 0, wlim);
+        gave_up = !one_wait(drain, 0, wlim) || !ok;
       }
     } else if (warp == 2) {
       // ---------------- decays: lane l takes rows 4 l .. 4 l + 3 of a chunk ----------------
@@ -309,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       double total = 0.0;
       if (chunks > 0) fetch(0);
-      for (int c = 0; c < chunks; ++c) {
+      int c = 0;
+      for (; c < chunks; ++c) {
         double G[4];
         float si[4];
         double sum = 0.0;
@@ -349,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&dec_full[c & 1]);
       }
+      gave_up = c < chunks;
       if (!outputs && lane == 0 && blk == 0) prm.seg.decay[bhs] = total;  // log2 of the segment's decay
     } else if (Lay::GATE && a.gate && outputs && lane == 0) {
       // ---------------- gate producer ----------------
@@ -361,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(smem + Lay::Z + x * kAtom, &tmZ, z_full, p0 + 64 * x, h, base + c * C, b);
       }
       if (!ok && c > 0) one_wait(z_full, uint32_t(c - 1) & 1u, wlim);
+      gave_up = !ok;
     }
   } else if (warp < 8) {
     if constexpr (Regs<NK>::SCORES < Regs<NK>::LAUNCH)
@@ -368,61 +412,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- scores: one row of the chunk per thread ----------------
     const int w = warp - 4, r = 32 * w + lane;
     const uint32_t lanes = uint32_t(32 * w) << 16;
-    for (int c = 0; outputs && c < chunks; ++c) {
-      const uint32_t ph = uint32_t(c) & 1u;
+    int c = 0;
+    for (; outputs && c < chunks; ++c) {
       const Decays &d = dec[c & 1];
       if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
       const float hi = d.hi[r], lo = d.lo[r];
-      if (!warp_wait(s_full, ph, wlim)) break;
+      if (!warp_wait(&s_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
       tc_fence_after();
       // Row r of warp w sees the whole blocks of 32 columns before block w, the part of its
       // own block up to its diagonal, and nothing behind.  A whole block's factors split at
       // the block's end, exp(G_r - G_end) and s_j exp(G_end - G_j), neither above one, so
       // only the diagonal block takes an exponential per element.
 #pragma unroll 1
-      for (int J = 0; J < 4; ++J) {
-        uint32_t pk[16];
+      for (int x0 = 0; x0 < C; x0 += 16) {  // 16 columns
+        uint32_t pk[8];
+        const int J = x0 >> 5;
         if (J > w) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+          for (int i = 0; i < 8; ++i) pk[i] = 0u;
         } else {
-          uint32_t sc[32];
-          tmem_ld32(tS + lanes + 32 * J, sc);
+          uint32_t sc[16];
+          tmem_ld16(tS + lanes + x0, sc);
           tmem_wait_ld();
           if (J < w) {
-          const float f = ex2_ftz((hi - d.hi[32 * J + 31]) + (lo - d.lo[32 * J + 31]));
-          const float2 f2 = make_float2(f, f);
+            const float f = ex2_ftz((hi - d.hi[32 * J + 31]) + (lo - d.lo[32 * J + 31]));
+            const float2 f2 = make_float2(f, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 cj = *reinterpret_cast<const float4 *>(&d.c[32 * J + 4 * i]);
-            const float2 x = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i]), __uint_as_float(sc[4 * i + 1])), f2),
-                                   make_float2(cj.x, cj.y));
-            const float2 y = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i + 2]), __uint_as_float(sc[4 * i + 3])), f2),
-                                   make_float2(cj.z, cj.w));
-            pk[2 * i] = pack_bf16x2(x.x, x.y);
-            pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
+            for (int i = 0; i < 4; ++i) {
+              const float4 cj = *reinterpret_cast<const float4 *>(&d.c[x0 + 4 * i]);
+              const float2 x = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i]), __uint_as_float(sc[4 * i + 1])), f2),
+                                     make_float2(cj.x, cj.y));
+              const float2 y = fmul2(fmul2(make_float2(__uint_as_float(sc[4 * i + 2]), __uint_as_float(sc[4 * i + 3])), f2),
+                                     make_float2(cj.z, cj.w));
+              pk[2 * i] = pack_bf16x2(x.x, x.y);
+              pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
+            }
+          } else {
+            const int last = r - x0;  // the diagonal
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 h4 = *reinterpret_cast<const float4 *>(&d.hi[x0 + 4 * i]);
+              const float4 l4 = *reinterpret_cast<const float4 *>(&d.lo[x0 + 4 * i]);
+              const float4 s4 = *reinterpret_cast<const float4 *>(&d.s[x0 + 4 * i]);
+              const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+              const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
+              float x[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                x[m] = 4 * i + m <= last
+                           ? __uint_as_float(sc[4 * i + m]) * (sj[m] * ex2_ftz((hi - hj[m]) + (lo - lj[m])))
+                           : 0.f;
+              pk[2 * i] = pack_bf16x2(x[0], x[1]);
+              pk[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+            }
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 h4 = *reinterpret_cast<const float4 *>(&d.hi[32 * J + 4 * i]);
-            const float4 l4 = *reinterpret_cast<const float4 *>(&d.lo[32 * J + 4 * i]);
-            const float4 s4 = *reinterpret_cast<const float4 *>(&d.s[32 * J + 4 * i]);
-            const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
-            const float sj[4] = {s4.x, s4.y, s4.z, s4.w};
-            float x[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              x[m] = 4 * i + m <= lane
-                         ? __uint_as_float(sc[4 * i + m]) * (sj[m] * ex2_ftz((hi - hj[m]) + (lo - lj[m])))
-                         : 0.f;
-            pk[2 * i] = pack_bf16x2(x[0], x[1]);
-            pk[2 * i + 1] = pack_bf16x2(x[2], x[3]);
-          }
-        }
         }
         // P over score columns that this row has read already
-        tmem_st16(tS + lanes + 16 * J, pk);
+        tmem_st8(tS + lanes + x0 / 2, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -432,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&dec_empty[c & 1]);
       }
     }
+    gave_up = outputs && c < chunks;
   } else if (warp >= 12 && warp < 20) {
     if constexpr (Regs<NK>::OUT < Regs<NK>::LAUNCH)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::OUT));
@@ -443,111 +490,145 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool skips = a.skip != nullptr, gates = a.gate != nullptr;
     // this row's 16-byte pieces of a 128-row tile
     const uint32_t row = (first >> 6) * kAtom + r * 128, p8 = (first & 63) >> 3, swz = r & 7;
-    // Rows are stored through shared memory 16 columns at a time, so that two lanes write the
-    // 32 contiguous bytes of a sector: this lane rows row0 and row0 + 16, columns half ..
-    const int half = 8 * (lane & 1), row0 = lane >> 1;
-    const int cols = pn - first - half;  // > 16 x: the lane's piece of group x exists
-    uint8_t *stage = smem + Lay::OUT + (warp - 12) * 1024;
-    const uint32_t put = lane * 32 + (((lane >> 2) & 1) << 4);
-    const uint32_t get = row0 * 32 + (((lane & 1) ^ ((row0 >> 2) & 1)) << 4);  // row0 + 16: the same bits
-    char *orow = reinterpret_cast<char *>(a.o) +
-                 2 * (b * a.o_batch + h * a.o_head + (base + 32 * w + row0) * a.o_row + p0 + first + half);
+    const int cols = pn - first;  // that exist
+    char *orow = reinterpret_cast<char *>(a.o) + 2 * (b * a.o_batch + h * a.o_head + (base + r) * a.o_row + p0 + first);
     const char *zrow = reinterpret_cast<const char *>(a.gate);
     if (gates) zrow += 2 * (b * a.gate_batch + h * a.gate_head + (base + r) * a.gate_row + p0 + first);
-    for (int c = 0; outputs && c < chunks; ++c) {
-      const uint32_t ph = uint32_t(c) & 1u;
+    // exp(G) Q S^T + skip v of chunk c, in place; P V is added to it
+    auto scale_rows = [&](int c) -> bool {
       const int st = c % ST;
-      const int rows = len - c * C - 32 * w;  // rows of this warp that count (may be none)
-      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
-      const float e = dec[c & 1].e[r];
-      if (Lay::GATE && gates && !warp_wait(z_full, ph, wlim)) break;
       const uint8_t *vs = smem + st * Lay::STAGE + Lay::V + row;
-      if (!warp_wait(o_full, ph, wlim)) break;
+      if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) return false;
+      const float e = dec[c & 1].e[r];
+      if (!warp_wait(&v_full[st], uint32_t(c / ST) & 1u, wlim) || !warp_wait(qs_done, uint32_t(c) & 1u, wlim)) return false;
       tc_fence_after();
       const float2 e2 = make_float2(e, e);
+      const uint32_t acc = tO + lanes + 128 * (c & 1);
 #pragma unroll 1
-      for (int x0 = 0; x0 < 4 * NV; x0 += 4) {  // 32 columns
-        uint4 z[4];
-        if (gates) {
+      for (int x = 0; x < kCols; x += 16) {
+        uint32_t o[16];
+        tmem_ld16(acc + x, o);
+        tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if constexpr (Lay::GATE) {
-              z[x] = *reinterpret_cast<const uint4 *>(smem + Lay::Z + row + (((p8 + x0 + x) ^ swz) << 4));
-            } else {
-              z[x] = make_uint4(0u, 0u, 0u, 0u);
-              if (lane < rows && 8 * (x0 + x) < pn - first) z[x] = __ldg(reinterpret_cast<const uint4 *>(zrow + 16 * (x0 + x)));
+        for (int i = 0; i < 16; i += 2) {
+          const float2 y = fmul2(e2, make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])));
+          o[i] = __float_as_uint(y.x);
+          o[i + 1] = __float_as_uint(y.y);
+        }
+        if (skips) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(vs + (((p8 + (x >> 3) + i) ^ swz) << 4));
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int m = 0; m < 4; m += 2) {
+              const float4 d = *reinterpret_cast<const float4 *>(&skip[x + 8 * i + 2 * m]);
+              uint32_t *y = o + 8 * i + 2 * m;
+              const float2 y0 = ffma2(make_float2(d.x, d.y), make_float2(bf16_lo(vw[m]), bf16_hi(vw[m])),
+                                      make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])));
+              const float2 y1 = ffma2(make_float2(d.z, d.w), make_float2(bf16_lo(vw[m + 1]), bf16_hi(vw[m + 1])),
+                                      make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])));
+              y[0] = __float_as_uint(y0.x);
+              y[1] = __float_as_uint(y0.y);
+              y[2] = __float_as_uint(y1.x);
+              y[3] = __float_as_uint(y1.y);
             }
           }
         }
+        tmem_st16(acc + x, o);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(x_full);
+        mbar_arrive(&v_empty[st]);
+        mbar_arrive(&dec_empty[c & 1]);
+      }
+      return true;
+    };
+    int c = outputs ? -1 : chunks;
+    for (; c < chunks; ++c) {
+      // the next chunk's Q S^T, ahead of this one's output
+      if (c + 1 < chunks && !scale_rows(c + 1)) break;
+      if (c < 0) continue;
+      const int rows = len - c * C - 32 * w;  // rows of this warp that count (may be none)
+      if (Lay::GATE && gates && !warp_wait(z_full, uint32_t(c) & 1u, wlim)) break;
+      if (!warp_wait(&o_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) break;
+      tc_fence_after();
+      const uint32_t acc = tO + lanes + 128 * (c & 1);
+#pragma unroll 1
+      for (int x = 0; x < kCols; x += 16) {
+        uint32_t o[16], out[8];
+        tmem_ld16(acc + x, o);
+        uint4 z[2];
+        if (gates) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {  // 8 columns: one piece of v, the gate and o
-          uint32_t o1[8], o2[8];
-          tmem_ld8(tO + lanes + 8 * (x0 + x), o1);
-          tmem_ld8(tX + lanes + 8 * (x0 + x), o2);
-          uint4 v = {};
-          if (skips) v = *reinterpret_cast<const uint4 *>(vs + (((p8 + x0 + x) ^ swz) << 4));
-          tmem_wait_ld();
-          uint32_t out[4];
-          const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, zw[4] = {z[x].x, z[x].y, z[x].z, z[x].w};
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (Lay::GATE) {
+              z[i] = *reinterpret_cast<const uint4 *>(smem + Lay::Z + row + (((p8 + (x >> 3) + i) ^ swz) << 4));
+            } else {
+              z[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (lane < rows && x + 8 * i < cols) z[i] = __ldg(reinterpret_cast<const uint4 *>(zrow + 2 * x + 16 * i));
+            }
+          }
+        }
+        tmem_wait_ld();
+        if (x == kCols - 16) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_empty[c & 1]);
+        }
+        const uint32_t zw[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // columns 2 i, 2 i + 1
-            float2 y = ffma2(e2, make_float2(__uint_as_float(o2[2 * i]), __uint_as_float(o2[2 * i + 1])),
-                             make_float2(__uint_as_float(o1[2 * i]), __uint_as_float(o1[2 * i + 1])));
-            if (skips)
-              y = ffma2(*reinterpret_cast<const float2 *>(&skip[8 * (x0 + x) + 2 * i]), make_float2(bf16_lo(vw[i]), bf16_hi(vw[i])), y);
-            if (gates) y = fmul2(y, make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
-            out[i] = pack_bf16x2(y.x, y.y);
+        for (int i = 0; i < 8; ++i) {  // columns x + 2 i, x + 2 i + 1
+          float2 y = make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          if (gates) y = fmul2(y, make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
+          out[i] = pack_bf16x2(y.x, y.y);
+        }
+        if (lane < rows && x < cols) {
+          char *dst = orow + 2 * x;
+          if (x + 8 < cols && (reinterpret_cast<uintptr_t>(dst) & 31) == 0) {  // a whole sector
+            st_global_v8(dst, out[0], out[1], out[2], out[3], out[4], out[5], out[6], out[7]);
+          } else {
+            st_global_v4(dst, out[0], out[1], out[2], out[3]);
+            if (x + 8 < cols) st_global_v4(dst + 16, out[4], out[5], out[6], out[7]);
           }
-          *reinterpret_cast<uint4 *>(stage + (put ^ (16 * (x & 1)))) = make_uint4(out[0], out[1], out[2], out[3]);
-          if (!(x & 1)) continue;
-          __syncwarp();
-          const uint4 a0 = *reinterpret_cast<const uint4 *>(stage + get), a1 = *reinterpret_cast<const uint4 *>(stage + get + 512);
-          if (8 * (x0 + x - 1) < cols) {
-            char *dst = orow + 16 * (x0 + x - 1);
-            if (row0 < rows) st_global_v4(dst, a0.x, a0.y, a0.z, a0.w);
-            if (row0 + 16 < rows) st_global_v4(dst + 32 * a.o_row, a1.x, a1.y, a1.z, a1.w);
-          }
-          __syncwarp();
         }
       }
-      tc_fence_before();
       __syncwarp();
       // Only here, behind the use of what was read: an arrival does not wait for loads that are
       // still on their way, and a tile released before them was overwritten under them.
-      if (lane == 0) {
-        mbar_arrive(o_empty);
-        mbar_arrive(&empty[st]);  // V
-        mbar_arrive(z_empty);
-        mbar_arrive(&dec_empty[c & 1]);
-      }
+      if (lane == 0) mbar_arrive(z_empty);
       if (gates) zrow += 2 * C * a.gate_row;
       orow += 2 * C * a.o_row;
     }
+    gave_up = c < chunks;
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NK>::KEYS));
     // ---------------- weighted keys: one row of the chunk per thread ----------------
     const int r = 32 * (warp - 8) + lane;
-    for (int c = 0; c < chunks; ++c) {
+    int c = 0;
+    for (; c < chunks; ++c) {
       const int st = c % ST;
       const uint32_t ph = uint32_t(c) & 1u;
       const int rem = len - c * C;
-      // Split over three buffers whose operands have been read: the high parts over the keys,
-      // the middle parts beside them, the low parts over the queries (the scores and Q S^T of
-      // this chunk and the state product of the last one are behind).
+      // Split over three buffers: the high parts over the keys, whose scores are done, the middle
+      // parts beside them, the low parts over the queries.  Q S^T of this chunk reads those, so
+      // the low parts of one atom wait in registers: only their stores come after it.
       if (!warp_wait(&dec_full[c & 1], uint32_t(c >> 1) & 1u, wlim) || !warp_wait(&full[st], uint32_t(c / ST) & 1u, wlim) ||
-          !warp_wait(c_full, ph ^ 1u, wlim) || (outputs && !warp_wait(qs_done, ph, wlim)))
+          !warp_wait(c_full, ph ^ 1u, wlim) || (outputs && !warp_wait(&s_full[c & 1], uint32_t(c >> 1) & 1u, wlim)) ||
+          (rem < C && !warp_wait(&v_full[st], uint32_t(c / ST) & 1u, wlim)))
         break;
       const float wj = dec[c & 1].w[r];
       uint8_t *krow = smem + st * Lay::STAGE + Lay::K + r * 128, *mrow = smem + Lay::MID + r * 128;
       uint8_t *qrow = smem + st * Lay::STAGE + Lay::Q + r * 128;
       const float2 w2 = make_float2(wj, wj);
-#pragma unroll 1
-      for (int x = 0; x < 8 * NK; ++x) {
-        const uint32_t off = (x >> 3) * kAtom + (((x & 7) ^ (r & 7)) << 4);
+      auto split = [&](uint32_t off, uint32_t *lo) {
         uint4 kk = *reinterpret_cast<const uint4 *>(krow + off);
         if (r >= rem) kk = make_uint4(0u, 0u, 0u, 0u);  // rows behind the sequence, whatever they hold
         const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
-        uint32_t hi[4], mid[4], lo[4];
+        uint32_t hi[4], mid[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float2 y = fmul2(w2, make_float2(bf16_lo(in[i]), bf16_hi(in[i])));
@@ -559,7 +640,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         *reinterpret_cast<uint4 *>(krow + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(mrow + off) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-        *reinterpret_cast<uint4 *>(qrow + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      };
+      uint32_t lo[32];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) split((x ^ (r & 7)) << 4, lo + 4 * x);
+      if (outputs && !warp_wait(qs_done, ph, wlim)) break;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        *reinterpret_cast<uint4 *>(qrow + ((x ^ (r & 7)) << 4)) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+      if constexpr (NK == 2) {
+#pragma unroll 2
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t off = kAtom + ((x ^ (r & 7)) << 4);
+          split(off, lo);
+          *reinterpret_cast<uint4 *>(qrow + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       if (r >= rem) {  // 0 * v must be 0 in the products
         uint8_t *vrow = smem + st * Lay::STAGE + Lay::V + r * 128;
@@ -572,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&dec_empty[c & 1]);
     }
+    gave_up = c < chunks;
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<NK>::STATE));
     // ---------------- state: one row of the state block per thread ----------------
@@ -607,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned t0 = (unsigned)clock();
         while (load_acquire(left) < 4u * seg)
           if ((unsigned)clock() - t0 > wlim) {
-            atomicOr(&g_err_lin, kErrTimeout);
             ok = false;
             break;
           }
@@ -631,9 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_state(prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense);
     for (int c = 0; ok && c < chunks; ++c) {
       const uint32_t ph = uint32_t(c) & 1u;
-      // the state as the operand of Q S^T: high and low bf16 parts.  The buffer's last reader,
-      // the chunk before's Q S^T, is behind its P V or its state product.
-      if (outputs && !warp_wait(qs_done, ph ^ 1u, wlim)) { ok = false; break; }
+      // The state as the operand of Q S^T: high and low bf16 parts.  The buffer's last reader,
+      // the Q S^T before, ran ahead of the state product that c_full told of.
       if (outputs && r < 64 * NV) {
         uint8_t *sb = smem + Lay::SB + r * 128;
 #pragma unroll
@@ -690,7 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) atomicAdd(left, 1u);
     }
+    gave_up = !ok && !failed;
   }
+  if (gave_up) atomicOr(&g_err_lin, kErrTimeout);
 
   tc_fence_before();
   __syncthreads();
@@ -768,8 +864,8 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
 // the rows are split into segments, as many as fit beside each other: the segments' own
 // states first (about 0.6 of a chunk's time each), then their outputs.  That takes 1.6 / n of
 // the time in n segments, and a second launch about as long as four chunks: 25 heads of 8320
-// rows 450 us whole and 163 us in five segments, 28 heads of 517 rows 18 us whole and 28 us
-// in two.
+// rows and dk 128 450 us whole and 163 us in five segments, 28 heads of 517 rows 18 us whole
+// and 28 us in two.
 //
 // More heads than SMs run in rounds, the last of which leaves SMs idle.  Then each head's rows
 // are a chain of segments that CTAs take up in turn, so that the rounds are shorter; a CTA's
