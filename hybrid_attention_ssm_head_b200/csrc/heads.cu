@@ -65,7 +65,7 @@ enum Partner {
 // Bound by instructions more than by HBM: per element a share of the conversions, of the
 // norm's sum over the head's lanes and of the rotation.  With a head's halves in lanes of
 // their own the rotation took eight shuffles per eight elements (109 us at 8 x 4224 rows of
-// 30 heads); a lane that holds both elements of its pairs needs none.
+// 30 heads of 64); a lane that holds both elements of its pairs needs none: 62 us, 4.2 TB/s.
 template <typename T, int PARTNER>
 __global__ void __launch_bounds__(32 * kHeadWarps)
     qk_norm_rope_kernel(const __grid_constant__ HeadsParams p) {

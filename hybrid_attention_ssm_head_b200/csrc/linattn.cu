@@ -352,9 +352,9 @@ LinearSegments scan_segments(const hymba_linear_attention &a) {
 }
 
 // Below this many rows a bf16 sequence is taken row by row: a chunk costs its 128 rows however
-// many count.  Row by row and in a chunk: 25 heads 9.6 and 10.5 us at 16 rows, 13.3 and 10.6 at
-// 24; 200 heads 13.4 and 21.3 us at 16, 21.1 and 21.1 at 32; 800 heads with dk 128 104 and 91 us
-// at 12 and 16, 129 and 91 at 16.
+// many count.  Row by row and in a chunk: 25 heads 10.3 and 11.1 us at 16 rows, 14.2 and 11.1 at
+// 24; 200 heads 14.1 and 22.1 us at 16, 22.7 and 21.9 at 32; 800 heads with dk 128 130 and 105 us
+// at 16 (row by row 105 at 12).
 constexpr int kFewRows = 16;
 bool on_tensor_cores(const hymba_linear_attention &a) { return a.dtype == HYMBA_BF16 && a.n_rows >= kFewRows; }
 LinearSegments segments_of(const hymba_linear_attention &a) {

@@ -864,13 +864,13 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
 // the rows are split into segments, as many as fit beside each other: the segments' own
 // states first (about 0.6 of a chunk's time each), then their outputs.  That takes 1.6 / n of
 // the time in n segments, and a second launch about as long as four chunks: 25 heads of 8320
-// rows and dk 128 450 us whole and 163 us in five segments, 28 heads of 517 rows 18 us whole
-// and 28 us in two.
+// rows 200 us whole and 88 us in five segments, with dk 128 379 and 157 us; 28 heads of 517 rows
+// 24 us whole and 30 us in two.
 //
 // More heads than SMs run in rounds, the last of which leaves SMs idle.  Then each head's rows
 // are a chain of segments that CTAs take up in turn, so that the rounds are shorter; a CTA's
-// start and end cost about as much as 0.7 of a chunk: 200 heads of 4224 rows 288 us whole and
-// 237 us in chains of two.
+// start and end cost about as much as 0.7 of a chunk.  200 heads of 4224 rows 234 us whole and
+// 206 us in chains of two, 180 heads with dk 128 399 and 314 us.
 LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a) {
   LinearSegments g{};
   const long long ctas = (long long)a.batch * a.n_heads * dv_blocks(a);
