@@ -114,7 +114,8 @@ struct Params {
 // issues in 43 % of the cycles, stalled on shared memory (which the operands of the products
 // and the tiles take for half of the time) and on each other; shortening the chain alone, by
 // buffers of its own for the low parts, made nothing faster.  HBM is at half of its rate: 400
-// heads of 8320 rows, dk 64, dv 128, 745 us for 401 us of bytes.
+// heads of 8320 rows, dk 64, dv 128, 745 us for 401 us of bytes (853 us in long runs, in which
+// the board's power holds the clock at 1.7 GHz).
 //   measured, 200 heads of 4224 rows / 25 of 8320 rows with dk 128 / 400 of 8320 rows:
 //     one output accumulator, 32 columns at a time                   237 / 170 / 842 us
 //     16 columns at a time (less code, fewer registers)              227 / 165 / 792 us
@@ -838,7 +839,8 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
   p.a = a;
   p.seg = seg;
   p.blocks = dv_blocks(a);
-  const long long cycles = wait_limit_cycles();
+  // A chain's waits are as long as a segment (about 50 cycles a row) when lengths differ.
+  const long long cycles = std::max<long long>(wait_limit_cycles(), seg.chain ? 500LL * seg.rows : 0);
   p.wlim = cycles > 0x7fffffffLL ? 0x7fffffffu : (unsigned)cycles;
   const long long ctas = (long long)a.batch * a.n_heads * p.blocks;
   if (ctas * seg.n > 0x7fffffffLL) {
@@ -887,10 +889,10 @@ LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a) {
     return g;
   }
   double best = 0.0;
-  for (int per = chunks; per >= 4; --per) {  // segments of at least four chunks
-    const int n = (chunks + per - 1) / per;
+  for (int want = 1; want <= std::min(32, std::max(1, chunks / 4)); ++want) {  // of at least four chunks
+    const int per = (chunks + want - 1) / want, n = (chunks + per - 1) / per;
     const double cost = (double)((ctas * n + 147) / 148) * (per + 0.7);
-    if (per == chunks || cost < 0.97 * best) {
+    if (want == 1 || cost < 0.97 * best) {
       best = cost;
       g.n = n;
       g.rows = per * C;

@@ -319,3 +319,51 @@ def test_repeated_calls_give_the_same_bits(dtype, B, L, H, K, dk, dv):
             first = o.clone(), S.clone()
         assert torch.equal(o, first[0]) and torch.equal(S, first[1]), i
     hy.hymba_stream_status(torch.cuda.current_stream())
+
+
+@pytest.mark.parametrize("dk,dv,pad,off", [(64, 128, 8, 0), (64, 72, 0, 8), (128, 40, 8, 8), (16, 16, 8, 24)])
+def test_outputs_off_sector_boundaries(dk, dv, pad, off):
+    """Rows of o that start 16 but not 32 bytes into a sector: the dense call's bits, and nothing beside them."""
+    B, L, H, K = 2, 300, 3, 1
+    x = inputs("bf16", B, L, H, K, dk, dv, lengths=[300, 77])
+    want, Sw = prefill(on_gpu(x), B, L, H, dv, dk)
+    wide = torch.full((B, L, H * (dv + pad) + 32), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = wide[:, :, off:off + H * (dv + pad)].unflatten(2, (H, dv + pad))[..., :dv]
+    got, S = prefill(on_gpu(x), B, L, H, dv, dk, o=o)
+    assert torch.equal(got, want) and torch.equal(S, Sw)
+    got.fill_(7.0)
+    assert bool((wide == 7.0).all())
+
+
+def test_chains_at_once_and_replayed():
+    """More heads than SMs: two calls at a time on streams of their own, then as a graph's replays."""
+    B, L, H, K, dk, dv = 6, 1030, 30, 2, 64, 64
+    x = inputs("bf16", B, L, H, K, dk, dv, lengths=[1030, 0, 1, 513, 1030, 900])
+    dev = on_gpu(x)
+    want = prefill(dev, B, L, H, dv, dk)
+    calls = []
+    for _ in range(2):
+        o = torch.full((B, L, H, dv), 7.0, dtype=torch.bfloat16, device="cuda")
+        S = torch.empty(B, H, dv, dk, device="cuda")
+        args = hy.make_linear_attention(o=o, state_out=S, **dev)
+        ws = torch.full((hy.hymba_linear_attention_workspace(args),), 255, dtype=torch.uint8, device="cuda")
+        assert ws.numel() > 0
+        calls.append((o, S, args, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o, S, args, ws, s in calls:
+            hy.hymba_linear_attention_prefill(args, ws, ws.numel(), s)
+    torch.cuda.synchronize()
+    hy.hymba_stream_status(torch.cuda.current_stream())
+    for o, S, *_ in calls:
+        assert torch.equal(o, want[0]) and torch.equal(S, want[1])
+    o, S, args, ws, s = calls[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        hy.hymba_linear_attention_prefill(args, ws, ws.numel(), torch.cuda.current_stream())
+    for _ in range(3):
+        o.fill_(7.0)
+        S.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(S, want[1])
