@@ -17,18 +17,18 @@ constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 struct HeadsParams {
   hymba_qk_norm_rope_args a;
-  int lanes;       // lanes per head: a power of two, 8 elements each
+  int lanes;       // lanes per head: a power of two, 2 N elements each
   int parts;       // units per row: the heads of a row are split over this many warps
   int chunk;       // loads (of 32 / lanes heads) a warp keeps in flight, at most kAhead
   unsigned units;  // batch * n_rows * parts
   double turns[kMaxPairs];  // f_i / (2 pi): turns per position
 };
 
-// Four elements of a head: 8 bytes of bf16, 16 of fp32.
-template <typename T>
-struct Vec4;
+// N elements of a head: 8 or 16 bytes of bf16, 16 of fp32.
+template <typename T, int N>
+struct Vec;
 template <>
-struct Vec4<__nv_bfloat16> {
+struct Vec<__nv_bfloat16, 4> {
   using R = uint2;
   static __device__ __forceinline__ void get(const R &r, float2 *x) {
     x[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
@@ -39,7 +39,21 @@ struct Vec4<__nv_bfloat16> {
   }
 };
 template <>
-struct Vec4<float> {
+struct Vec<__nv_bfloat16, 8> {
+  using R = uint4;
+  static __device__ __forceinline__ void get(const R &r, float2 *x) {
+    x[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+    x[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+    x[2] = make_float2(bf16_lo(r.z), bf16_hi(r.z));
+    x[3] = make_float2(bf16_lo(r.w), bf16_hi(r.w));
+  }
+  static __device__ __forceinline__ R put(const float2 *x) {
+    return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                      pack_bf16x2(x[3].x, x[3].y));
+  }
+};
+template <>
+struct Vec<float, 4> {
   using R = float4;
   static __device__ __forceinline__ void get(const R &r, float2 *x) {
     x[0] = make_float2(r.x, r.y);
@@ -48,12 +62,12 @@ struct Vec4<float> {
   static __device__ __forceinline__ R put(const float2 *x) { return make_float4(x[0].x, x[0].y, x[1].x, x[1].y); }
 };
 
-// Which eight elements of a head a lane holds, and where an element's pair is.
+// Which 2 N elements of a head a lane holds, and where an element's pair is.
 enum Partner {
-  kNone,    // no rotation: elements 8 l ..
-  kPairs,   // pairs (2i, 2i+1): elements 8 l .., four pairs
-  kHalves,  // halves of the whole head: elements 4 l .. and d/2 + 4 l .., four pairs
-  kShared   // halves of a part of the head: elements 8 l .., the pairs through shared memory
+  kNone,    // no rotation: elements 2 N l ..
+  kPairs,   // pairs (2i, 2i+1): elements 2 N l .., N pairs
+  kHalves,  // halves of the whole head: elements N l .. and d/2 + N l .., N pairs
+  kShared   // halves of a part of the head: elements 2 N l .., the pairs through shared memory
 };
 
 // A warp takes one unit: a row of a sequence and a share of its heads.  Its lanes first
@@ -65,15 +79,18 @@ enum Partner {
 // Bound by instructions more than by HBM: per element a share of the conversions, of the
 // norm's sum over the head's lanes and of the rotation.  With a head's halves in lanes of
 // their own the rotation took eight shuffles per eight elements (109 us at 8 x 4224 rows of
-// 30 heads of 64); a lane that holds both elements of its pairs needs none: 62 us, 4.2 TB/s.
-template <typename T, int PARTNER>
+// 30 heads of 64); a lane that holds both elements of its pairs needs none (62 us), and with
+// sixteen elements a lane the sums' shuffles are a third (57 us, 4.6 TB/s).  Not kept: loads two
+// or three ahead (59, 64 us), the first loads ahead of the angles (66 us with eight elements),
+// registers cut for more warps (61 us).
+template <typename T, int PARTNER, int N>
 __global__ void __launch_bounds__(32 * kHeadWarps)
     qk_norm_rope_kernel(const __grid_constant__ HeadsParams p) {
   pdl_wait();
   pdl_trigger();
-  using V = Vec4<T>;
+  using V = Vec<T, N>;
   __shared__ float2 s_trig[PARTNER == kNone ? 1 : kHeadWarps * kMaxPairs];
-  __shared__ float s_stage[PARTNER == kShared ? kHeadWarps * 256 : 1];
+  __shared__ float s_stage[PARTNER == kShared ? kHeadWarps * 64 * N : 1];
   const hymba_qk_norm_rope_args &a = p.a;
   const int warp = warp_id(), lane = lane_id();
   const unsigned unit = blockIdx.x * kHeadWarps + warp;
@@ -83,9 +100,9 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   const int b = int(row_id / (unsigned)a.n_rows), r = int(row_id - b * (unsigned)a.n_rows);
   const int lanes = p.lanes, li = lane & (lanes - 1), slot = lane / lanes, per = 32 / lanes;
   const int d = a.head_dim, rot = a.rope.dim, half = rot >> 1;
-  const bool live = 8 * li < d;
-  // the lane's elements: four from e0, four from e1
-  const int e0 = PARTNER == kHalves ? 4 * li : 8 * li, e1 = PARTNER == kHalves ? half + 4 * li : e0 + 4;
+  const bool live = 2 * N * li < d;
+  // the lane's elements: N from e0, N from e1
+  const int e0 = PARTNER == kHalves ? N * li : 2 * N * li, e1 = PARTNER == kHalves ? half + N * li : e0 + N;
 
   const int nq = a.q.n_heads, heads = nq + a.k.n_heads;
   const int groups = (heads + per - 1) / per;
@@ -95,8 +112,8 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   T *qo = reinterpret_cast<T *>(a.q.out) + b * a.q.out_batch + r * a.q.out_row;
   T *ko = reinterpret_cast<T *>(a.k.out) + b * a.k.out_batch + r * a.k.out_row;
 
-  // kPairs, kHalves: cos and sin of the lane's four pairs; kShared: of its eight elements'
-  constexpr int NF = PARTNER == kNone ? 1 : PARTNER == kShared ? 8 : 4;
+  // kPairs, kHalves: cos and sin of the lane's N pairs; kShared: of its elements'
+  constexpr int NF = PARTNER == kNone ? 1 : PARTNER == kShared ? 2 * N : N;
   float cs[NF], sn[NF];
   if constexpr (PARTNER != kNone) {
     const double pos = double(a.pos0 + (a.positions ? a.positions[row_id] : (long long)r));
@@ -111,7 +128,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      const int i = PARTNER == kPairs ? 4 * li + j : PARTNER == kHalves ? e0 + j : e0 + j < half ? e0 + j : e0 + j - half;
+      const int i = PARTNER == kPairs ? N * li + j : PARTNER == kHalves ? e0 + j : e0 + j < half ? e0 + j : e0 + j - half;
       const float2 t = i < half ? trig[i] : make_float2(1.f, 0.f);  // behind the rotated part
       cs[j] = t.x;
       sn[j] = PARTNER == kShared && e0 + j < half ? -t.y : t.y;
@@ -135,74 +152,76 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
       if (u >= p.chunk || g0 + u >= groups) break;  // the same for the whole warp
       const int hh = (g0 + u) * per + slot;
       // elements two by two: e0, e0 + 1 | .. | e1 + 2, e1 + 3
-      float2 x[4];
+      float2 x[N];
       V::get(ra[u], x);
-      V::get(rb[u], x + 2);
+      V::get(rb[u], x + N / 2);
       if (a.norm) {
-        const float2 s2 = ffma2(x[3], x[3], ffma2(x[2], x[2], ffma2(x[1], x[1], fmul2(x[0], x[0]))));
+        float2 s2 = fmul2(x[0], x[0]);
+#pragma unroll
+        for (int j = 1; j < N; ++j) s2 = ffma2(x[j], x[j], s2);
         float ss = s2.x + s2.y;
         for (int m = lanes >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = fmul2(x[j], make_float2(inv, inv));
+        for (int j = 0; j < N; ++j) x[j] = fmul2(x[j], make_float2(inv, inv));
         const float *weight = hh < nq ? a.q.weight : a.k.weight;
         if (weight && live) {
-          const float4 w0 = __ldg(reinterpret_cast<const float4 *>(weight + e0));
-          const float4 w1 = __ldg(reinterpret_cast<const float4 *>(weight + e1));
-          x[0] = fmul2(x[0], make_float2(w0.x, w0.y));
-          x[1] = fmul2(x[1], make_float2(w0.z, w0.w));
-          x[2] = fmul2(x[2], make_float2(w1.x, w1.y));
-          x[3] = fmul2(x[3], make_float2(w1.z, w1.w));
+#pragma unroll
+          for (int j = 0; j < N; j += 2) {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(weight + (2 * j < N ? e0 + 2 * j : e1 + 2 * j - N)));
+            x[j] = fmul2(x[j], make_float2(w.x, w.y));
+            x[j + 1] = fmul2(x[j + 1], make_float2(w.z, w.w));
+          }
         }
       }
-      float2 y[4];
+      float2 y[N];
       if constexpr (PARTNER == kNone) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = x[j];
+        for (int j = 0; j < N; ++j) y[j] = x[j];
       } else if constexpr (PARTNER == kPairs) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < N; ++j) {
           y[j] = make_float2(fmaf(x[j].x, cs[j], -x[j].y * sn[j]), fmaf(x[j].y, cs[j], x[j].x * sn[j]));
           if (e0 + 2 * j >= rot) y[j] = x[j];  // not rotated: as it is, whatever its pair holds
         }
       } else if constexpr (PARTNER == kHalves) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < N / 2; ++j) {
           const float2 c2 = make_float2(cs[2 * j], cs[2 * j + 1]), s2 = make_float2(sn[2 * j], sn[2 * j + 1]);
           const float2 n2 = make_float2(-s2.x, -s2.y);
-          y[j] = ffma2(x[j], c2, fmul2(x[j + 2], n2));
-          y[j + 2] = ffma2(x[j + 2], c2, fmul2(x[j], s2));
+          y[j] = ffma2(x[j], c2, fmul2(x[j + N / 2], n2));
+          y[j + N / 2] = ffma2(x[j + N / 2], c2, fmul2(x[j], s2));
         }
       } else {
-        // each lane's eight elements at 8 lane: the warp's heads side by side
-        float *st = s_stage + warp * 256;
+        // each lane's elements at 2 N lane: the warp's heads side by side
+        float *st = s_stage + warp * 64 * N;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<float2 *>(&st[8 * lane + 2 * j]) = x[j];
+        for (int j = 0; j < N; ++j) *reinterpret_cast<float2 *>(&st[2 * N * lane + 2 * j]) = x[j];
         __syncwarp();
         auto turn = [&](float v, int j) {
           const int e = e0 + j, other = e < half ? e + half : e - half;
-          return e < rot ? fmaf(v, cs[j], st[8 * (lane - li) + other] * sn[j]) : v;
+          return e < rot ? fmaf(v, cs[j], st[2 * N * (lane - li) + other] * sn[j]) : v;
         };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = make_float2(turn(x[j].x, 2 * j), turn(x[j].y, 2 * j + 1));
+        for (int j = 0; j < N; ++j) y[j] = make_float2(turn(x[j].x, 2 * j), turn(x[j].y, 2 * j + 1));
       }
       if (live && hh < heads) {
         T *dst = hh < nq ? qo + hh * a.q.out_head : ko + (hh - nq) * a.k.out_head;
         *reinterpret_cast<typename V::R *>(dst + e0) = V::put(y);
-        *reinterpret_cast<typename V::R *>(dst + e1) = V::put(y + 2);
+        *reinterpret_cast<typename V::R *>(dst + e1) = V::put(y + N / 2);
       }
     }
   }
 }
 
-template <typename T>
+template <typename T, int N>
 void heads_launch(const HeadsParams &p, int partner, dim3 g, cudaStream_t s) {
   const dim3 blk(32 * kHeadWarps);
-  if (partner == kNone) launch_kernel(qk_norm_rope_kernel<T, kNone>, g, blk, 0, s, p);
-  else if (partner == kPairs) launch_kernel(qk_norm_rope_kernel<T, kPairs>, g, blk, 0, s, p);
-  else if (partner == kHalves) launch_kernel(qk_norm_rope_kernel<T, kHalves>, g, blk, 0, s, p);
-  else launch_kernel(qk_norm_rope_kernel<T, kShared>, g, blk, 0, s, p);
+  if (partner == kNone) launch_kernel(qk_norm_rope_kernel<T, kNone, N>, g, blk, 0, s, p);
+  else if (partner == kPairs) launch_kernel(qk_norm_rope_kernel<T, kPairs, N>, g, blk, 0, s, p);
+  else if (partner == kHalves) launch_kernel(qk_norm_rope_kernel<T, kHalves, N>, g, blk, 0, s, p);
+  else launch_kernel(qk_norm_rope_kernel<T, kShared, 4>, g, blk, 0, s, p);
 }
 
 }  // namespace
@@ -210,8 +229,6 @@ void heads_launch(const HeadsParams &p, int partner, dim3 g, cudaStream_t s) {
 hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
   HeadsParams p;
   p.a = a;
-  p.lanes = 1;
-  while (p.lanes * 8 < a.head_dim) p.lanes *= 2;
   const int half = a.rope.dim / 2;
   for (int i = 0; i < half; ++i) {
     const double f = pow(a.rope.base, -2.0 * i / a.rope.dim);
@@ -229,6 +246,12 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
   const int partner = half == 0 ? kNone
                       : a.rope.layout == HYMBA_ROPE_PAIRS ? kPairs
                       : a.rope.dim == a.head_dim ? kHalves : kShared;
+  // Sixteen elements a lane where the type and the head's size allow 16-byte loads: fewer lanes
+  // share a sum and fewer loads go out (8 x 4224 rows of 30 heads 57 us, with eight 62 us).  A
+  // part's halves go through shared memory, eight elements a lane.
+  const int n = a.dtype == HYMBA_BF16 && partner != kShared && a.head_dim % 16 == 0 ? 8 : 4;
+  p.lanes = 1;
+  while (p.lanes * 2 * n < a.head_dim) p.lanes *= 2;
   // One warp per row amortises the row's angles over all of its heads; with too few rows to
   // give every SM 16 warps, a row's heads are split over several warps, down to one load of
   // 32 / lanes heads each.  (A warp over the same row of several sequences, which could share
@@ -247,8 +270,9 @@ hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
   }
   p.units = (unsigned)units;
   const dim3 grid((unsigned)((units + kHeadWarps - 1) / kHeadWarps));
-  if (a.dtype == HYMBA_BF16) heads_launch<__nv_bfloat16>(p, partner, grid, s);
-  else heads_launch<float>(p, partner, grid, s);
+  if (n == 8) heads_launch<__nv_bfloat16, 8>(p, partner, grid, s);
+  else if (a.dtype == HYMBA_BF16) heads_launch<__nv_bfloat16, 4>(p, partner, grid, s);
+  else heads_launch<float, 4>(p, partner, grid, s);
   note_launch(1);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

@@ -36,6 +36,12 @@ CASES = [
     ("bf16", 1, 33, 2, 2, 256, 256, "halves", "wavelength", True, True, True),
     ("bf16", 1, 3, 2, 0, 256, 250, "halves", "none", False, False, False),
     ("bf16", 2, 3, 0, 5, 64, 0, "pairs", "none", True, True, False),      # norm alone, keys alone
+    ("bf16", 2, 70, 3, 2, 16, 16, "halves", "none", True, True, False),   # one lane of 16 elements per head
+    ("bf16", 2, 70, 3, 2, 48, 22, "pairs", "none", True, True, True),     # the last lanes idle, a pair border inside a lane
+    ("bf16", 2, 7, 9, 4, 72, 72, "halves", "none", True, True, False),    # 8 elements a lane
+    ("bf16", 2, 7, 9, 4, 88, 88, "pairs", "none", True, True, False),
+    ("bf16", 3, 40, 11, 2, 240, 240, "halves", "linear", True, True, True),
+    ("bf16", 2, 7, 9, 4, 80, 0, "pairs", "none", True, True, False),
     ("f32", 2, 5, 6, 3, 128, 40, "pairs", "linear", False, False, True),
     ("f32", 2, 17, 25, 5, 64, 64, "halves", "wavelength", True, True, False),
     ("f32", 1, 4, 3, 1, 256, 64, "pairs", "none", True, True, True),
