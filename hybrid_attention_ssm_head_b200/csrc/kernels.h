@@ -335,6 +335,8 @@ struct LinearSegments {
   unsigned *ticket;  // chain: [1 + batch * n_heads * dv blocks] zeroed: the next segment to
                      // take, and how many warps have left each chain's state
 };
+// Between the passes: each segment's slot then holds the state after it.
+void linear_prefix(const hymba_linear_attention &a, const LinearSegments &g, cudaStream_t s);
 // ... of bf16 storage on the tensor cores.
 LinearSegments linear_attention_tc_segments(const hymba_linear_attention &a);
 size_t linear_attention_tc_tickets(const hymba_linear_attention &a);  // words of a chain's tickets

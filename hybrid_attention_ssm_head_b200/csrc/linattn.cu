@@ -140,7 +140,15 @@ constexpr int kScanState = 64;  // state rows per CTA (two per thread group)
 
 // NC columns of two adjacent state rows per thread, CL threads per row pair: the state stays
 // in registers as fp32 pairs.  q, k, v, the gate and the decays of kScanRows rows are staged
-// in shared memory as fp32.
+// in shared memory as fp32, the next rows' waiting in registers meanwhile.
+//
+// Bound by the latency of one row after another.  Neighbouring threads take neighbouring pieces
+// of four columns, so that a warp's reads of k and q meet no bank twice.  5 heads of 4000 fp32
+// rows with dk 128 / 8 heads of 1031 with dk 64 / 800 heads of 15 bf16 rows with dk 128:
+//   NC columns of a thread side by side                        398 / 58 / 130 us
+//   pieces in turn                                             148 / 55 / 44 us
+//   next rows' loads and decays ahead; 16 columns for dk <= 64   137 / 46 / 50 us
+// (16 columns for dk 128 as well: 165 us before the last step.)
 //
 // Decays near one: a fp32 decay is off by up to 2^-25, the same way at every row of a head
 // with one fixed decay, so their product drifts from exp(sum g) by 2^-25 times the rows.
@@ -154,14 +162,14 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
   constexpr int THR = kScanState / 2 * CL, DK = NC * CL;
   static_assert(THR >= 32, "one warp stages the decays");
   __shared__ __align__(16) float s_q[kScanRows][DK], s_k[kScanRows][DK];
-  __shared__ __align__(8) float s_v[kScanRows][kScanState], s_z[kScanRows][kScanState];
+  __shared__ __align__(16) float s_v[kScanRows][kScanState], s_z[kScanRows][kScanState];
   __shared__ float2 s_dx[kScanRows];  // (decay, input scale)
   const int blocks = (a.dv + kScanState - 1) / kScanState;
   const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, seg = blockIdx.x / blocks;
   const int hk = h / (a.n_heads / a.n_qk_heads);
   const int pb = (blockIdx.x % blocks) * kScanState;   // the CTA's first state row
   const int pn = min(kScanState, a.dv - pb);           // and how many (even)
-  const int pr = 2 * (tid / CL), c0 = (tid % CL) * NC; // this thread's row pair and columns
+  const int pr = 2 * (tid / CL), c0 = 4 * (tid % CL);  // this thread's row pair and columns c0 + CL c ..
   const bool rows_live = pr < pn;
   const bool outputs = g.pass == 1;                    // else the segment's state alone
   const int L = min(linear_length(a, b), (seg + 1) * g.rows);
@@ -179,35 +187,29 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
   for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int c = 0; c < NC / 2; ++c) S[r][c] = make_float2(0.f, 0.f);
-  // The state the segment starts from: the call's, or the earlier segments' own states, each
-  // decayed by those after it (a segment's own state starts from zero, the first one's from
-  // the call's).
+  // The state the segment starts from: the call's, or (outputs) the one after the segments
+  // before it; a segment's own state starts from zero, the first one's from the call's.
   const float *from = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
   if (outputs && g.n > 1) from = a.state_in ? g.state + ((g.n - 1) * heads + bh) * dense : nullptr;
-  const int first = outputs ? 0 : seg;
-  for (int j = first; j <= seg; ++j) {
-    const float *src = j > first ? g.state + ((j - 1) * heads + bh) * dense : seg == 0 ? from : nullptr;
-    if (!src || !rows_live) continue;
-    const float keep = j > first ? exp2f((float)g.decay[(j - 1) * heads + bh]) : 0.f;
-    const float2 k2 = make_float2(keep, keep);
+  if (seg > 0) from = outputs ? g.state + ((seg - 1) * heads + bh) * dense : nullptr;
+  if (from && rows_live)
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int c = 0; c < NC; c += 4)
-        if (c0 + c < a.dk) {
-          const float4 x = *reinterpret_cast<const float4 *>(src + (long long)(pb + pr + r) * a.dk + c0 + c);
-          S[r][c / 2] = ffma2(k2, S[r][c / 2], make_float2(x.x, x.y));
-          S[r][c / 2 + 1] = ffma2(k2, S[r][c / 2 + 1], make_float2(x.z, x.w));
+        if (c0 + CL * c < a.dk) {
+          const float4 x = *reinterpret_cast<const float4 *>(from + (long long)(pb + pr + r) * a.dk + c0 + CL * c);
+          S[r][c / 2] = make_float2(x.x, x.y);
+          S[r][c / 2 + 1] = make_float2(x.z, x.w);
         }
-  }
   auto store_state = [&](float *dst) {
     if (!rows_live) return;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int c = 0; c < NC; c += 4)
-        if (c0 + c < a.dk)
-          *reinterpret_cast<float4 *>(dst + (long long)(pb + pr + r) * a.dk + c0 + c) =
+        if (c0 + CL * c < a.dk)
+          *reinterpret_cast<float4 *>(dst + (long long)(pb + pr + r) * a.dk + c0 + CL * c) =
               make_float4(S[r][c / 2].x, S[r][c / 2].y, S[r][c / 2 + 1].x, S[r][c / 2 + 1].y);
   };
   if (!outputs && seg == 0 && a.state_in)  // a copy for the outputs' pass, which may write in place
@@ -217,31 +219,39 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
 
   double carry = 1.0;  // exp(sum g) over the product of the decays used so far
   double total = 0.0;  // log2 of this lane's rows' decays
-  for (int t0 = seg * g.rows; t0 < L; t0 += kScanRows) {
-    const int nt = min(kScanRows, L - t0);
-    __syncthreads();
-    for (int i = tid; i < nt * (DK / 4); i += THR) {
-      const int t = i / (DK / 4), c = 4 * (i % (DK / 4));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (c < a.dk) {
-        if (outputs) x = load4(qp + (t0 + t) * a.q_row + c);
-        y = load4(kp + (t0 + t) * a.k_row + c);
-      }
-      *reinterpret_cast<float4 *>(&s_q[t][c]) = x;
-      *reinterpret_cast<float4 *>(&s_k[t][c]) = y;
+  // The next rows wait in registers while these are computed.
+  constexpr int QN = kScanRows * (DK / 4) / THR, VN = kScanRows * (kScanState / 4) / THR;
+  float4 rq[QN], rk[QN], rv[VN], rz[VN];
+  float2 dx_next = make_float2(0.f, 0.f);
+  auto fetch = [&](int t0) {
+    const int nt = min(kScanRows, L - t0), t = tid;  // the first warp: one row's decay a lane
+    float gt = 0.f, st = 1.f;
+    if (t < nt) {
+      if (gp) gt = gp[(t0 + t) * a.decay_row];
+      if (sp) st = sp[(t0 + t) * a.scale_row];
     }
-    for (int i = tid; i < nt * (kScanState / 4); i += THR) {
-      const int t = i / (kScanState / 4), c = 4 * (i % (kScanState / 4));
-      if (c < pn) {
-        *reinterpret_cast<float4 *>(&s_v[t][c]) = load4(vp + (t0 + t) * a.v_row + c);
-        if (outputs && a.gate) *reinterpret_cast<float4 *>(&s_z[t][c]) = load4(zp + (t0 + t) * a.gate_row + c);
+#pragma unroll
+    for (int u = 0; u < QN; ++u) {
+      const int i = tid + u * THR, r = i / (DK / 4), c = 4 * (i % (DK / 4));
+      rq[u] = rk[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nt && c < a.dk) {
+        if (outputs) rq[u] = load4(qp + (t0 + r) * a.q_row + c);
+        rk[u] = load4(kp + (t0 + r) * a.k_row + c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < VN; ++u) {
+      const int i = tid + u * THR, r = i / (kScanState / 4), c = 4 * (i % (kScanState / 4));
+      rv[u] = rz[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nt && c < pn) {
+        rv[u] = load4(vp + (t0 + r) * a.v_row + c);
+        if (outputs && a.gate) rz[u] = load4(zp + (t0 + r) * a.gate_row + c);
       }
     }
     if (tid < 32) {
-      const int t = tid;
       double want = 1.0;
       if (t < nt && gp) {
-        const float gt = linear_log_decay(gp[(t0 + t) * a.decay_row]);
+        gt = linear_log_decay(gt);
         want = exp((double)gt);
         total += (double)gt * 1.4426950408889634074;
       }
@@ -261,9 +271,28 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
         }
         carry = __shfl_sync(0xffffffffu, next, f);
       }
-      if (t < nt) s_dx[t] = make_float2(used, sp ? sp[(t0 + t) * a.scale_row] : 1.f);
+      dx_next = make_float2(used, st);
     }
+  };
+  if (seg * g.rows < L) fetch(seg * g.rows);
+  for (int t0 = seg * g.rows; t0 < L; t0 += kScanRows) {
+    const int nt = min(kScanRows, L - t0);
     __syncthreads();
+#pragma unroll
+    for (int u = 0; u < QN; ++u) {
+      const int i = tid + u * THR, r = i / (DK / 4), c = 4 * (i % (DK / 4));
+      *reinterpret_cast<float4 *>(&s_q[r][c]) = rq[u];
+      *reinterpret_cast<float4 *>(&s_k[r][c]) = rk[u];
+    }
+#pragma unroll
+    for (int u = 0; u < VN; ++u) {
+      const int i = tid + u * THR, r = i / (kScanState / 4), c = 4 * (i % (kScanState / 4));
+      *reinterpret_cast<float4 *>(&s_v[r][c]) = rv[u];
+      *reinterpret_cast<float4 *>(&s_z[r][c]) = rz[u];
+    }
+    if (tid < kScanRows) s_dx[tid] = dx_next;
+    __syncthreads();
+    if (t0 + kScanRows < L) fetch(t0 + kScanRows);
     for (int t = 0; t < nt; ++t) {
       const float2 dx = s_dx[t];
       const float2 v = *reinterpret_cast<const float2 *>(&s_v[t][pr]);
@@ -272,26 +301,29 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
       float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
       for (int c = 0; c < NC; c += 4) {
-        const float4 k = *reinterpret_cast<const float4 *>(&s_k[t][c0 + c]);
-        const float4 q = *reinterpret_cast<const float4 *>(&s_q[t][c0 + c]);
+        const float4 k = *reinterpret_cast<const float4 *>(&s_k[t][c0 + CL * c]);
+        const float4 q = *reinterpret_cast<const float4 *>(&s_q[t][c0 + CL * c]);
         const float2 ka = make_float2(k.x, k.y), kb = make_float2(k.z, k.w);
         const float2 qa = make_float2(q.x, q.y), qb = make_float2(q.z, q.w);
         S[0][c / 2] = ffma2(d2, S[0][c / 2], fmul2(x0, ka));
         S[0][c / 2 + 1] = ffma2(d2, S[0][c / 2 + 1], fmul2(x0, kb));
         S[1][c / 2] = ffma2(d2, S[1][c / 2], fmul2(x1, ka));
         S[1][c / 2 + 1] = ffma2(d2, S[1][c / 2 + 1], fmul2(x1, kb));
-        acc0 = ffma2(S[0][c / 2], qa, acc0);
-        acc1 = ffma2(S[1][c / 2], qa, acc1);
-        acc0 = ffma2(S[0][c / 2 + 1], qb, acc0);
-        acc1 = ffma2(S[1][c / 2 + 1], qb, acc1);
+        if (outputs) {
+          acc0 = ffma2(S[0][c / 2], qa, acc0);
+          acc1 = ffma2(S[1][c / 2], qa, acc1);
+          acc0 = ffma2(S[0][c / 2 + 1], qb, acc0);
+          acc1 = ffma2(S[1][c / 2 + 1], qb, acc1);
+        }
       }
+      if (!outputs) continue;
       float y0 = acc0.x + acc0.y, y1 = acc1.x + acc1.y;
 #pragma unroll
       for (int m = CL >> 1; m > 0; m >>= 1) {
         y0 += __shfl_xor_sync(0xffffffffu, y0, m);
         y1 += __shfl_xor_sync(0xffffffffu, y1, m);
       }
-      if (outputs && tid % CL == 0 && rows_live) {
+      if (tid % CL == 0 && rows_live) {
         y0 = fmaf(skip.x, v.x, a.scale * y0);
         y1 = fmaf(skip.y, v.y, a.scale * y1);
         if (a.gate) {
@@ -317,6 +349,38 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
   }
 }
 
+// The segments' own states to the states after them, in place: P_j = decay_j P_{j-1} + own_j.
+// One thread takes four elements through all segments, eight of them requested at a time.
+// Read and written once: with the sum taken where it is used, each segment over those before
+// it, 5 heads of 4000 fp32 rows of 128 x 128 states in 84 segments took 716 us, so 398 us (136 us with the later steps).
+__global__ void __launch_bounds__(256) linear_prefix_kernel(const __grid_constant__ LinearSegments g, long long size, long long heads) {
+  pdl_wait();
+  pdl_trigger();
+  const long long bh = blockIdx.y + (long long)blockIdx.z * gridDim.y;
+  const long long e = 4 * (blockIdx.x * 256ll + threadIdx.x);
+  if (e >= size || bh >= heads) return;
+  const long long step = heads * size;
+  float *p = g.state + bh * size + e;
+  const double *d = g.decay + bh;
+  float4 S = *reinterpret_cast<const float4 *>(p);
+  for (int j = 1; j < g.n - 1; j += 8) {
+    float4 x[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j + u < g.n - 1) {
+        x[u] = *reinterpret_cast<const float4 *>(p + (j + u) * step);
+        w[u] = exp2f((float)d[(j + u) * heads]);
+      }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j + u < g.n - 1) {
+        S = make_float4(fmaf(w[u], S.x, x[u].x), fmaf(w[u], S.y, x[u].y), fmaf(w[u], S.z, x[u].z), fmaf(w[u], S.w, x[u].w));
+        *reinterpret_cast<float4 *>(p + (j + u) * step) = S;
+      }
+  }
+}
+
 hymba_status launched(const char *what) {
   note_launch(1);
   const cudaError_t e = cudaGetLastError();
@@ -331,10 +395,11 @@ template <typename T>
 void scan_launch(const hymba_linear_attention &a, LinearSegments g, cudaStream_t s) {
   constexpr int one = kScanState / 2;
   for (g.pass = g.n > 1 ? 0 : 1; g.pass < 2; ++g.pass) {
+    if (g.pass == 1) linear_prefix(a, g, s);
     const dim3 grid((a.dv + kScanState - 1) / kScanState * (g.pass ? g.n : g.n - 1), a.n_heads, a.batch);
     if (a.dk <= 16) launch_kernel(linear_scan_kernel<T, 16, 1>, grid, dim3(one), 0, s, a, g);
-    else if (a.dk <= 32) launch_kernel(linear_scan_kernel<T, 32, 1>, grid, dim3(one), 0, s, a, g);
-    else if (a.dk <= 64) launch_kernel(linear_scan_kernel<T, 32, 2>, grid, dim3(2 * one), 0, s, a, g);
+    else if (a.dk <= 32) launch_kernel(linear_scan_kernel<T, 16, 2>, grid, dim3(2 * one), 0, s, a, g);
+    else if (a.dk <= 64) launch_kernel(linear_scan_kernel<T, 16, 4>, grid, dim3(4 * one), 0, s, a, g);
     else launch_kernel(linear_scan_kernel<T, 32, 4>, grid, dim3(4 * one), 0, s, a, g);
     note_launch(1);
   }
@@ -352,11 +417,12 @@ LinearSegments scan_segments(const hymba_linear_attention &a) {
 }
 
 // Below this many rows a bf16 sequence is taken row by row: a chunk costs its 128 rows however
-// many count.  Row by row and in a chunk: 25 heads 10.3 and 11.1 us at 16 rows, 14.2 and 11.1 at
-// 24; 200 heads 14.1 and 22.1 us at 16, 22.7 and 21.9 at 32; 800 heads with dk 128 130 and 105 us
-// at 16 (row by row 105 at 12).
-constexpr int kFewRows = 16;
-bool on_tensor_cores(const hymba_linear_attention &a) { return a.dtype == HYMBA_BF16 && a.n_rows >= kFewRows; }
+// many count.  Row by row and in a chunk, dk 64: 25 heads 9.8 and 12.1 us at 24 rows, 12.0 and
+// 12.2 at 32, 16.9 and 12.1 at 48; 200 heads 17.5 and 23.9 us at 32, 24.2 and 23.8 at 48; dk 128:
+// 25 heads 16.5 and 18.3 us at 32, 800 heads 90 and 104 us at 32, 128 and 105 at 48; dk 16, 16
+// heads: 7.5 and 7.7 us at 16, 10.7 and 7.7 at 24.
+int few_rows(const hymba_linear_attention &a) { return a.dk > 32 ? 32 : 16; }
+bool on_tensor_cores(const hymba_linear_attention &a) { return a.dtype == HYMBA_BF16 && a.n_rows >= few_rows(a); }
 LinearSegments segments_of(const hymba_linear_attention &a) {
   return on_tensor_cores(a) ? linear_attention_tc_segments(a) : scan_segments(a);
 }
@@ -369,6 +435,14 @@ size_t segment_rest_bytes(const hymba_linear_attention &a, const LinearSegments 
 }
 
 }  // namespace
+
+void linear_prefix(const hymba_linear_attention &a, const LinearSegments &g, cudaStream_t s) {
+  if (g.n < 3 || g.chain) return;
+  const long long size = (long long)a.dv * a.dk;
+  launch_kernel(linear_prefix_kernel, dim3((unsigned)((size / 4 + 255) / 256), a.n_heads, a.batch), dim3(256), 0, s, g, size,
+                (long long)a.batch * a.n_heads);
+  note_launch(1);
+}
 
 hymba_status linear_attention_step(const hymba_linear_attention &a, cudaStream_t s) {
   int lanes = 2;

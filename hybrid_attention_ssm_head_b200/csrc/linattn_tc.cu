@@ -680,23 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int n = 0; n < 32 * NK; ++n) S[n] = make_float2(0.f, 0.f);
     const long long at = (long long)(p0 + r) * a.dk;  // this row in a head's state
-    // S = keep * S + the row at src
-    auto add_row = [&](const float *src, float keep) {
-#pragma unroll
-      for (int n = 0; n < 64 * NK; n += 4)
-        if (mine && n < a.dk) {
-          const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + at + n));  // other SMs' stores among them
-          S[n / 2] = ffma2(make_float2(keep, keep), S[n / 2], make_float2(x.x, x.y));
-          S[n / 2 + 1] = ffma2(make_float2(keep, keep), S[n / 2 + 1], make_float2(x.z, x.w));
-        }
-    };
-    // The state the segment starts from: the sequence's first one, or the earlier segments'
-    // own states, each decayed by those after it.
+    // The state the segment starts from: the call's, or (outputs) the one after the segments
+    // before it; a segment's own state starts from zero, the first one's from the call's.
     const long long heads = (long long)a.batch * a.n_heads;
     const float *from = a.state_in ? a.state_in + b * a.state_in_batch + h * dense : nullptr;
     if (outputs && prm.seg.n > 1 && !prm.seg.chain)
       from = a.state_in ? prm.seg.state + ((prm.seg.n - 1) * heads + bh) * dense : nullptr;
-    const int first = outputs && !prm.seg.chain ? 0 : seg;  // a segment's own state starts from zero
+    if (seg > 0) from = outputs ? prm.seg.state + ((prm.seg.chain ? 0 : seg - 1) * heads + bh) * dense : nullptr;
     unsigned *left = prm.seg.ticket + 1 + bh * prm.blocks + blk;  // chain: four warps for each segment
     bool ok = !failed;
     if (prm.seg.chain && seg > 0) {
@@ -709,14 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
       ok = __all_sync(0xffffffffu, ok);
-      from = prm.seg.state + bh * dense;
     }
-#pragma unroll 1
-    for (int j = first; j <= seg; ++j) {
-      const bool start = j == first;
-      const float *src = !start ? prm.seg.state + ((j - 1) * heads + bh) * dense : seg == 0 || prm.seg.chain ? from : nullptr;
-      if (ok && src) add_row(src, start ? 0.f : exp2f((float)prm.seg.decay[(j - 1) * heads + bh]));
-    }
+    if (ok && from && mine)
+#pragma unroll
+      for (int n = 0; n < 64 * NK; n += 4)
+        if (n < a.dk) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(from + at + n));  // other SMs' stores among them
+          S[n / 2] = make_float2(x.x, x.y);
+          S[n / 2 + 1] = make_float2(x.z, x.w);
+        }
     auto store_state = [&](float *dst) {
 #pragma unroll
       for (int n = 0; n < 64 * NK; n += 4)
@@ -848,6 +839,7 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
     return HYMBA_ERR_UNSUPPORTED;
   }
   for (p.seg.pass = seg.n > 1 && !seg.chain ? 0 : 1; p.seg.pass < 2; ++p.seg.pass) {
+    if (p.seg.pass == 1) linear_prefix(a, p.seg, s);
     const long long grid = ctas * (p.seg.pass ? seg.n : seg.n - 1);
     launch_kernel(linear_chunk_kernel<NK, NV>, dim3((unsigned)grid), dim3(kThreads), (size_t)Lay::TOTAL, s, tq, tk, tv, tz, p);
     note_launch(1);
