@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
 // The segments' own states to the states after them, in place: P_j = decay_j P_{j-1} + own_j.
 // One thread takes four elements through all segments, eight of them requested at a time.
 // Read and written once: with the sum taken where it is used, each segment over those before
-// it, 5 heads of 4000 fp32 rows of 128 x 128 states in 84 segments took 716 us, so 398 us (136 us with the later steps).
+// it, 5 heads of 4000 fp32 rows of 128 x 128 states in 84 segments took 716 us, so 398 us (124 us with the later steps).
 __global__ void __launch_bounds__(256) linear_prefix_kernel(const __grid_constant__ LinearSegments g, long long size, long long heads) {
   pdl_wait();
   pdl_trigger();
@@ -405,12 +405,13 @@ void scan_launch(const hymba_linear_attention &a, LinearSegments g, cudaStream_t
   }
 }
 
-// Few heads of many rows: segments of at least 32 rows, about eight CTAs for each SM (2 x 4 heads
-// of 1031 fp32 rows: 433 us whole, 82 us so).
+// Few heads of many rows: segments of at least 32 rows, about three CTAs for each SM, as many as
+// run beside each other.  Whole / so / with eight for each SM: 2 x 4 heads of 1031 fp32 rows 282 /
+// 46 / 46 us, 50 heads of 2000 rows with dk 64 588 / 361 / 398 us, 200 heads 826 / 826 / 1122 us.
 LinearSegments scan_segments(const hymba_linear_attention &a) {
   LinearSegments g{};
   const long long ctas = (long long)a.batch * a.n_heads * ((a.dv + kScanState - 1) / kScanState);
-  const long long want = std::max<long long>(1, std::min<long long>(8 * 148 / std::max<long long>(1, ctas), a.n_rows / 32));
+  const long long want = std::max<long long>(1, std::min<long long>(3 * 148 / std::max<long long>(1, ctas), a.n_rows / 32));
   g.rows = (int)(((a.n_rows + want - 1) / want + kScanRows - 1) / kScanRows * kScanRows);
   g.n = (a.n_rows + g.rows - 1) / g.rows;
   return g;
