@@ -265,8 +265,8 @@ def _run_own(c):
         if "call" not in c:  # the description of its buffers and of the rotation that a program fills in once
             rope = hy.make_rope(c["rot"], c["layout"], scaling=c["scaling"], **ROPE[c["scaling"]])
             c["call"] = hy.make_qk_norm_rope(c["q"], c["k"], c["q_out"], c["k_out"], norm=c["norm"], eps=1e-6,
-                                             q_weight=c["wq"], k_weight=c["wk"], rope=rope, pos0=c["pos0"],
-                                             positions=c["positions"])
+                                             q_weight=c["wq"], k_weight=c["wk"], rope=rope,
+                                             pos0=0 if c["given"] else c["pos0"], positions=c["positions"])
         hy.hymba_qk_norm_rope(c["call"], stream)
         return c["q_out"], c["k_out"]
     if "call" not in c:  # the description of its buffers and the workspace that a program keeps
