@@ -11,7 +11,7 @@ namespace hymba {
 namespace {
 
 constexpr int kHeadWarps = 4;
-constexpr int kAhead = 4;
+constexpr int kAhead = 4;       // loads in flight of a warp that takes several
 constexpr int kMaxPairs = 128;  // head_dim <= 256
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
@@ -83,7 +83,7 @@ enum Partner {
 // sixteen elements a lane the sums' shuffles are a third (57 us, 4.6 TB/s).  Not kept: loads two
 // or three ahead (59, 64 us), the first loads ahead of the angles (66 us with eight elements),
 // registers cut for more warps (61 us).
-template <typename T, int PARTNER, int N>
+template <typename T, int PARTNER, int N, int AHEAD>
 __global__ void __launch_bounds__(32 * kHeadWarps)
     qk_norm_rope_kernel(const __grid_constant__ HeadsParams p) {
   pdl_wait();
@@ -112,6 +112,21 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   T *qo = reinterpret_cast<T *>(a.q.out) + b * a.q.out_batch + r * a.q.out_row;
   T *ko = reinterpret_cast<T *>(a.k.out) + b * a.k.out_batch + r * a.k.out_row;
 
+  typename V::R ra[AHEAD], rb[AHEAD];
+  auto request = [&](int g0) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int hh = (g0 + u) * per + slot;
+      ra[u] = rb[u] = typename V::R{};
+      if (live && u < p.chunk && hh < heads) {
+        const T *src = hh < nq ? qi + hh * a.q.in_head : ki + (hh - nq) * a.k.in_head;
+        ra[u] = *reinterpret_cast<const typename V::R *>(src + e0);
+        rb[u] = *reinterpret_cast<const typename V::R *>(src + e1);
+      }
+    }
+  };
+  if constexpr (AHEAD == 1) request(part);
+
   // kPairs, kHalves: cos and sin of the lane's N pairs; kShared: of its elements'
   constexpr int NF = PARTNER == kNone ? 1 : PARTNER == kShared ? 2 * N : N;
   float cs[NF], sn[NF];
@@ -136,19 +151,9 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   }
 
   for (int g0 = part * p.chunk; g0 < groups; g0 += p.parts * p.chunk) {
-    typename V::R ra[kAhead], rb[kAhead];
+    if constexpr (AHEAD > 1) request(g0);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int hh = (g0 + u) * per + slot;
-      ra[u] = rb[u] = typename V::R{};
-      if (live && u < p.chunk && hh < heads) {
-        const T *src = hh < nq ? qi + hh * a.q.in_head : ki + (hh - nq) * a.k.in_head;
-        ra[u] = *reinterpret_cast<const typename V::R *>(src + e0);
-        rb[u] = *reinterpret_cast<const typename V::R *>(src + e1);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       if (u >= p.chunk || g0 + u >= groups) break;  // the same for the whole warp
       const int hh = (g0 + u) * per + slot;
       // elements two by two: e0, e0 + 1 | .. | e1 + 2, e1 + 3
@@ -215,13 +220,21 @@ __global__ void __launch_bounds__(32 * kHeadWarps)
   }
 }
 
+template <typename T, int N, int AHEAD>
+void heads_launch_ahead(const HeadsParams &p, int partner, dim3 g, cudaStream_t s) {
+  const dim3 blk(32 * kHeadWarps);
+  if (partner == kNone) launch_kernel(qk_norm_rope_kernel<T, kNone, N, AHEAD>, g, blk, 0, s, p);
+  else if (partner == kPairs) launch_kernel(qk_norm_rope_kernel<T, kPairs, N, AHEAD>, g, blk, 0, s, p);
+  else if (partner == kHalves) launch_kernel(qk_norm_rope_kernel<T, kHalves, N, AHEAD>, g, blk, 0, s, p);
+  else launch_kernel(qk_norm_rope_kernel<T, kShared, 4, AHEAD>, g, blk, 0, s, p);
+}
+// A warp whose share of a row is one load requests it ahead of the angles and holds no more:
+// 40 x 2976 rows of 6 heads of 48 71 us, as with several loads 114 us; 3 tokens of 30 heads 2.6 and
+// 2.9 us.  With two loads a warp the registers for both cost more (57 to 66 us at 30 heads).
 template <typename T, int N>
 void heads_launch(const HeadsParams &p, int partner, dim3 g, cudaStream_t s) {
-  const dim3 blk(32 * kHeadWarps);
-  if (partner == kNone) launch_kernel(qk_norm_rope_kernel<T, kNone, N>, g, blk, 0, s, p);
-  else if (partner == kPairs) launch_kernel(qk_norm_rope_kernel<T, kPairs, N>, g, blk, 0, s, p);
-  else if (partner == kHalves) launch_kernel(qk_norm_rope_kernel<T, kHalves, N>, g, blk, 0, s, p);
-  else launch_kernel(qk_norm_rope_kernel<T, kShared, 4>, g, blk, 0, s, p);
+  if (p.chunk == 1) heads_launch_ahead<T, N, 1>(p, partner, g, s);
+  else heads_launch_ahead<T, N, kAhead>(p, partner, g, s);
 }
 
 }  // namespace
