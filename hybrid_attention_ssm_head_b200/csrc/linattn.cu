@@ -148,7 +148,8 @@ constexpr int kScanState = 64;  // state rows per CTA (two per thread group)
 //   NC columns of a thread side by side                        398 / 58 / 130 us
 //   pieces in turn                                             148 / 55 / 44 us
 //   next rows' loads and decays ahead; 16 columns for dk <= 64   137 / 46 / 50 us
-// (16 columns for dk 128 as well: 165 us before the last step.)
+// (16 columns for dk 128 as well: 165 us before the last step.)  24 columns up to dk 96: 32 heads
+// of 7006 rows with dk 80 1077 us, with 32 columns 1323 us.
 //
 // Decays near one: a fp32 decay is off by up to 2^-25, the same way at every row of a head
 // with one fixed decay, so their product drifts from exp(sum g) by 2^-25 times the rows.
@@ -400,6 +401,7 @@ void scan_launch(const hymba_linear_attention &a, LinearSegments g, cudaStream_t
     if (a.dk <= 16) launch_kernel(linear_scan_kernel<T, 16, 1>, grid, dim3(one), 0, s, a, g);
     else if (a.dk <= 32) launch_kernel(linear_scan_kernel<T, 16, 2>, grid, dim3(2 * one), 0, s, a, g);
     else if (a.dk <= 64) launch_kernel(linear_scan_kernel<T, 16, 4>, grid, dim3(4 * one), 0, s, a, g);
+    else if (a.dk <= 96) launch_kernel(linear_scan_kernel<T, 24, 4>, grid, dim3(4 * one), 0, s, a, g);
     else launch_kernel(linear_scan_kernel<T, 32, 4>, grid, dim3(4 * one), 0, s, a, g);
     note_launch(1);
   }

@@ -92,6 +92,8 @@ CASES = [
     ("f32", 2, 1, 4, 1, 64, 128, "token", True, True, None),
     ("f32", 2, 33, 4, 2, 64, 128, "token", True, True, None),
     ("f32", 1, 200, 3, 1, 128, 72, "head", True, True, None),
+    ("f32", 2, 150, 4, 2, 80, 96, "head", True, True, [150, 77]),
+    ("f32", 1, 700, 2, 1, 96, 24, "token", True, True, None),
     ("f32", 2, 70, 2, 2, 16, 256, "token", False, False, None),
     ("f32", 1, 50, 2, 1, 40, 8, "none", True, True, None),
     ("f32", 1, 90, 2, 1, 32, 64, "strong", True, True, None),
