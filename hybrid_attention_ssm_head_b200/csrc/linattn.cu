@@ -2,6 +2,7 @@
 //   S_t = exp(g_t) S_{t-1} + s_t v_t k_t^T,   o_t = (scale S_t q_t + skip v_t) gate_t
 // The state S [dv, dk] is fp32 throughout.
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "linattn.cuh"
@@ -154,7 +155,10 @@ constexpr int kScanState = 64;  // state rows per CTA (two per thread group)
 // Decays near one: a fp32 decay is off by up to 2^-25, the same way at every row of a head
 // with one fixed decay, so their product drifts from exp(sum g) by 2^-25 times the rows.
 // The staged decays are therefore corrected every kFix rows: exp(sum g) over the product used
-// so far is carried in fp64, and the next group's first decay takes it up.
+// so far is carried in fp64, and the next group's first decay takes it up.  Only decays in fp32's
+// normal range take part: the ratio of a smaller one is up to 1.4 or 0.5, and would scale the rows
+// added since.  Behind such a decay nothing of the state before it is left that a ratio could
+// put right, so the ratio carried so far ends there too.
 template <typename T, int NC, int CL>
 __global__ void __launch_bounds__(kScanState / 2 * CL)
     linear_scan_kernel(const __grid_constant__ hymba_linear_attention a, const __grid_constant__ LinearSegments g) {
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
       float used = (float)want;
       // what the rounding of the other rows of this group of kFix leaves over; then each
       // group's first decay in turn takes up what was left over before it
-      double left = t % kFix && used > 0.f ? want / (double)used : 1.0;
+      double left = t % kFix && used >= FLT_MIN ? want / (double)used : 1.0;
 #pragma unroll
       for (int m = kFix >> 1; m > 0; m >>= 1) left *= __shfl_xor_sync(0xffffffffu, left, m);
 #pragma unroll
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kScanState / 2 * CL)
         if (t == f) {
           const double exact = want * carry;
           used = (float)exact;
-          next = (used > 0.f ? exact / (double)used : 1.0) * left;
+          next = (used >= FLT_MIN ? exact / (double)used : 1.0) * left;
         }
         carry = __shfl_sync(0xffffffffu, next, f);
       }

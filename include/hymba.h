@@ -447,6 +447,8 @@ HYMBA_API hymba_status hymba_qk_norm_rope(const hymba_qk_norm_rope_args *args, h
  *   log_decay  g [batch, n_rows, n_heads] fp32, any strides >= 0 (0 repeats a value: one decay
  *              for each head), or NULL (no decay).  g <= 0; below -110, -infinity included,
  *              the state is forgotten (exp(g) is 0 in fp32), as at the start of a document.
+ *              Between -87 and -110 exp(g) is below fp32's normal range: what it leaves of the
+ *              state keeps few bits or none.
  *   in_scale   s, likewise, or NULL (1)
  *   skip       [n_heads, dv] fp32 or NULL (0)
  *   state_in   S_0, each sequence's [n_heads, dv, dk] dense, state_in_batch floats apart (0: one
