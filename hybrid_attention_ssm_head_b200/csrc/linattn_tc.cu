@@ -363,13 +363,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           si[i] = s[i];
         }
         if (c + 1 < chunks) fetch(c + 1);
-        double before = sum;  // inclusive scan of the lanes' sums, then exclusive
+        // The sum before the lane's rows: the lane below's inclusive one.  (Not the lane's own less
+        // its rows: a NaN among those would reach the ones before it.)
+        double before = sum;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
           const double o = __shfl_up_sync(0xffffffffu, before, m);
           if (lane >= m) before += o;
         }
-        before -= sum;
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 0) before = 0.0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) G[i] += before;
         const double end = __shfl_sync(0xffffffffu, G[3], 31);

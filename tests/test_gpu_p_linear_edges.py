@@ -24,3 +24,24 @@ def test_decays_below_the_normal_range_scale_nothing_behind_them(dtype, L, row):
     x["v"][:, row:row + 3] *= 64
     o, S = prefill(on_gpu(x), 1, L, 6, 64, 64)
     check(x, o, S, dtype)
+
+
+@pytest.mark.parametrize("dtype,B,L,H,dk", [("bf16", 1, 300, 2, 64), ("bf16", 1, 30, 2, 64), ("f32", 1, 300, 2, 64),
+                                            ("bf16", 1, 300, 2, 128)])
+@pytest.mark.parametrize("name", ["log_decay", "in_scale", "q", "k", "gate"])
+@pytest.mark.parametrize("t", [3, 7, 27])
+def test_a_non_finite_value_reaches_no_row_before_its_own(name, t, dtype, B, L, H, dk):
+    """NaN in the last of four rows, of the first sequence's first head: the rows before it and the other
+    head, where it shares no row with the first, keep their bits."""
+    x = inputs(dtype, B, L, H, H, dk, 64)
+    clean, _ = prefill(on_gpu(x), B, L, H, 64, dk)
+    for at in (t, L - 5):  # again in the last rows, which the last chunk holds
+        bad = {**x, name: x[name].clone()}
+        bad[name][0, at, 0] = float("nan")
+        o, _ = prefill(on_gpu(bad), B, L, H, 64, dk)
+        assert torch.equal(o[:, :at], clean[:, :at]) and torch.equal(o[:, :, 1:], clean[:, :, 1:])
+        assert bool(o[0, at, 0].isnan().all())
+        if name in ("log_decay", "in_scale", "k"):  # they reach the state
+            assert bool(o[0, at:, 0].isnan().all())
+        else:
+            assert torch.equal(o[0, at + 1:], clean[0, at + 1:])
