@@ -242,6 +242,10 @@ void heads_launch(const HeadsParams &p, int partner, dim3 g, cudaStream_t s) {
 hymba_status qk_norm_rope(const hymba_qk_norm_rope_args &a, cudaStream_t s) {
   HeadsParams p;
   p.a = a;
+  // A side without heads holds nothing that may be read: the slots of a row's last load behind its
+  // last head pick the keys' weight.
+  if (a.q.n_heads == 0) p.a.q = hymba_head_rows{};
+  if (a.k.n_heads == 0) p.a.k = hymba_head_rows{};
   const int half = a.rope.dim / 2;
   for (int i = 0; i < half; ++i) {
     const double f = pow(a.rope.base, -2.0 * i / a.rope.dim);
