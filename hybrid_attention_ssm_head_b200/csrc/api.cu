@@ -10,7 +10,9 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -97,12 +99,18 @@ struct BranchStreams {
   bool ready = false;
 };
 
+// What a consumer has to know of its producer at every call.  Held by both, so that it is there
+// when the producer's handle is gone.
+struct LayerMark {
+  uint64_t id;
+  hymba_rope rope;  // hymba_layer_set_heads' (dim 0: none)
+};
+
 struct hymba_layer {
   hymba_layer_config cfg;
   hymba_layer_weights w;
-  uint64_t id;
-  const hymba_layer *producer;  // non-null for a K/V-sharing consumer
-  uint64_t producer_id;
+  std::shared_ptr<LayerMark> mark;
+  std::shared_ptr<const LayerMark> producer;  // non-null for a K/V-sharing consumer
   BranchStreams br;
   bool heads_on = false;         // hymba_layer_set_heads
   hymba_layer_heads heads = {};
@@ -235,12 +243,17 @@ hymba_status hymba_layer_create(const hymba_layer_config *cfg, const hymba_layer
     if (!p) FAIL(HYMBA_ERR_INVALID_ARG, "null weight pointer");
     if (!aligned16(p)) FAIL(HYMBA_ERR_INVALID_ARG, "weight pointer not 16-byte aligned");
   }
-  hymba_layer *L = new hymba_layer;
+  hymba_layer *L = new (std::nothrow) hymba_layer;
+  if (!L) FAIL(HYMBA_ERR_DEVICE, "out of host memory");
+  try {
+    L->mark = std::make_shared<LayerMark>();
+  } catch (const std::bad_alloc &) {
+    delete L;
+    FAIL(HYMBA_ERR_DEVICE, "out of host memory");
+  }
   L->cfg = c;
   L->w = *w;
-  L->id = g_next_id.fetch_add(1);
-  L->producer = nullptr;
-  L->producer_id = 0;
+  L->mark->id = g_next_id.fetch_add(1);
   // the concurrent prefill's side stream, on the current device (retried at the first
   // prefill where no device was usable here)
   if (c.branch_chunks >= 2) branch_create(L->br);
@@ -268,8 +281,7 @@ hymba_status hymba_kv_share_bind(hymba_layer *consumer, const hymba_layer *produ
       c.rope_base != p.rope_base)
     FAIL(HYMBA_ERR_NOT_BOUND, "producer and consumer differ in heads, head dims, n_meta, window, "
                               "global flag, dtype or rotary base");
-  consumer->producer = producer;
-  consumer->producer_id = producer->id;
+  consumer->producer = producer->mark;
   return HYMBA_OK;
 }
 
@@ -281,6 +293,7 @@ hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *
   if (!layer) FAIL(HYMBA_ERR_INVALID_ARG, "null layer");
   if (!heads) {
     layer->heads_on = false;
+    layer->mark->rope = hymba_rope{};
     return HYMBA_OK;
   }
   const hymba_layer_config &c = layer->cfg;
@@ -294,6 +307,7 @@ hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *
     FAIL(HYMBA_ERR_INVALID_ARG, "weight pointer not 16-byte aligned");
   layer->heads = *heads;
   layer->heads_on = true;
+  layer->mark->rope = heads->rope;
   return HYMBA_OK;
 }
 
@@ -319,9 +333,8 @@ hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hymba_linear
 
 // A consumer reads keys at its producer's positions: both must rotate alike.
 static hymba_status check_rotation(const hymba_layer *layer) {
-  const hymba_layer *p = layer->producer;
-  if (!p || p->id != layer->producer_id) return HYMBA_OK;  // a stale producer is reported by its stamp
-  const hymba_rope a = layer->heads_on ? layer->heads.rope : hymba_rope{}, b = p->heads_on ? p->heads.rope : hymba_rope{};
+  if (!layer->producer) return HYMBA_OK;
+  const hymba_rope &a = layer->mark->rope, &b = layer->producer->rope;
   bool same = a.dim == b.dim;
   if (same && a.dim > 0) {
     same = a.layout == b.layout && a.scaling == b.scaling && a.base == b.base && a.attn_factor == b.attn_factor;
@@ -889,10 +902,10 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
     a.window = c.window;
     a.is_global = c.is_global;
     if ((st = kv_cache_emit(a, c.dtype, stream)) != HYMBA_OK) return st;
-    kv_cache->owner = layer->id;
+    kv_cache->owner = layer->mark->id;
   }
   if (!consumer) {
-    kv->owner = layer->id;
+    kv->owner = layer->mark->id;
     kv->batch = batch;
     kv->rows = L;
   }
@@ -908,7 +921,7 @@ static hymba_status check_prefill_kv(const hymba_layer *layer, int batch, int L,
   if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v))
     FAIL(HYMBA_ERR_INVALID_ARG, "kv buffers null or misaligned");
   if (consumer) {
-    if (kv->owner != layer->producer_id || layer->producer->id != layer->producer_id)
+    if (kv->owner != layer->producer->id)
       FAIL(HYMBA_ERR_NOT_BOUND, "kv was not written by this consumer's producer");
     if (kv->batch != batch || kv->rows != L)
       FAIL(HYMBA_ERR_NOT_BOUND, "producer K/V has batch %d rows %d, consumer needs %d x %d",
@@ -977,7 +990,7 @@ hymba_status hymba_layer_meta_precompute(hymba_layer *layer, const void *x_meta,
     FAIL(HYMBA_ERR_INVALID_ARG, "meta cache y/h/conv null or misaligned");
   hymba_kv_seq kv{};
   if (consumer) {
-    if (!producer_meta || producer_meta->owner != layer->producer_id)
+    if (!producer_meta || producer_meta->owner != layer->producer->id)
       FAIL(HYMBA_ERR_NOT_BOUND, "a consumer needs its producer's meta cache");
     kv.k = producer_meta->k;
     kv.v = producer_meta->v;
@@ -1008,7 +1021,7 @@ hymba_status hymba_layer_meta_precompute(hymba_layer *layer, const void *x_meta,
   r.meta = true;
   st = prefill_run(layer, 1, r, &kv, nullptr, &ssm, workspace, lay, reinterpret_cast<cudaStream_t>(stream));
   if (st != HYMBA_OK) return st;
-  meta->owner = layer->id;
+  meta->owner = layer->mark->id;
   return HYMBA_OK;
 }
 
@@ -1040,7 +1053,7 @@ hymba_status hymba_layer_prefill_cached(hymba_layer *layer, int batch, int n_tok
   if (st != HYMBA_OK) return st;
   const int L = c.n_meta + n_tokens;
   if (!x || !y || !aligned16(x) || !aligned16(y)) FAIL(HYMBA_ERR_INVALID_ARG, "x/y null or misaligned");
-  if (!meta || meta->owner != layer->id) FAIL(HYMBA_ERR_NOT_BOUND, "meta cache not computed by this layer");
+  if (!meta || meta->owner != layer->mark->id) FAIL(HYMBA_ERR_NOT_BOUND, "meta cache not computed by this layer");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     FAIL(HYMBA_ERR_INVALID_ARG, "workspace null or not 256-byte aligned");
   if (workspace_bytes < lay.total)
@@ -1141,9 +1154,9 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
   const long long need = c.is_global ? pos + 1 : (long long)c.n_meta + c.window;
   if (kv_cache->capacity < need)
     FAIL(HYMBA_ERR_INVALID_ARG, "kv_cache capacity %d < %lld", kv_cache->capacity, need);
-  if (consumer && kv_cache->owner != layer->producer_id)
+  if (consumer && kv_cache->owner != layer->producer->id)
     FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache is not this consumer's producer's store");
-  if (!consumer && kv_cache->owner != 0 && kv_cache->owner != layer->id)
+  if (!consumer && kv_cache->owner != 0 && kv_cache->owner != layer->mark->id)
     FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache belongs to another layer");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     FAIL(HYMBA_ERR_INVALID_ARG, "workspace null or not 256-byte aligned");
@@ -1362,7 +1375,7 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
     g.epi.nseg = 1;
     if ((st = gemm_decode(g, c.dtype, stream)) != HYMBA_OK) return st;
   }
-  if (!consumer) kv_cache->owner = layer->id;
+  if (!consumer) kv_cache->owner = layer->mark->id;
   return HYMBA_OK;
 }
 

@@ -169,7 +169,8 @@ HYMBA_API int hymba_layer_is_consumer(const hymba_layer *layer);
  * written by `producer`.  Host only.  Checks that n_kv_heads, head dims,
  * n_meta, window and is_global match, that the producer is not itself a
  * consumer, and that the consumer's W_in width is the consumer width;
- * returns NOT_BOUND / INVALID_ARG otherwise.  Binding twice rebinds. */
+ * returns NOT_BOUND / INVALID_ARG otherwise.  Binding twice rebinds.  The producer's
+ * handle may be destroyed before the consumer's: K/V that it wrote stay readable. */
 HYMBA_API hymba_status hymba_kv_share_bind(hymba_layer *consumer, const hymba_layer *producer);
 
 /* ---- prefill ------------------------------------------------------------ */
