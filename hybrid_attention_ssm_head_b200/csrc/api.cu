@@ -103,6 +103,8 @@ struct BranchStreams {
 // when the producer's handle is gone.
 struct LayerMark {
   uint64_t id;
+  uint64_t stamp;   // of the data the handle writes: id, or another one for every setting of its
+                    // head operators, under which keys and states are others
   hymba_rope rope;  // hymba_layer_set_heads' (dim 0: none)
 };
 
@@ -253,7 +255,7 @@ hymba_status hymba_layer_create(const hymba_layer_config *cfg, const hymba_layer
   }
   L->cfg = c;
   L->w = *w;
-  L->mark->id = g_next_id.fetch_add(1);
+  L->mark->id = L->mark->stamp = g_next_id.fetch_add(1);
   // the concurrent prefill's side stream, on the current device (retried at the first
   // prefill where no device was usable here)
   if (c.branch_chunks >= 2) branch_create(L->br);
@@ -288,12 +290,29 @@ hymba_status hymba_kv_share_bind(hymba_layer *consumer, const hymba_layer *produ
 // ---------------------------------------------------------------------------
 // operators inside the layer
 // ---------------------------------------------------------------------------
+static bool same_rope(const hymba_rope &a, const hymba_rope &b) {
+  if (a.dim != b.dim) return false;
+  if (a.dim == 0) return true;
+  if (a.layout != b.layout || a.scaling != b.scaling || a.base != b.base || a.attn_factor != b.attn_factor) return false;
+  if (a.scaling != HYMBA_ROPE_SCALE_NONE && a.factor != b.factor) return false;
+  return a.scaling != HYMBA_ROPE_SCALE_WAVELENGTH ||
+         (a.orig_len == b.orig_len && a.low_turns == b.low_turns && a.high_turns == b.high_turns);
+}
+
+// After a change of the head operators: what was stored before holds other keys, or states of
+// another size.  Without them it is what the handle wrote without them before.
+static void restamp(hymba_layer *layer) {
+  layer->mark->stamp = layer->heads_on || layer->linear_on ? g_next_id.fetch_add(1) : layer->mark->id;
+}
+
 hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *heads) {
   g_msg[0] = 0;
   if (!layer) FAIL(HYMBA_ERR_INVALID_ARG, "null layer");
   if (!heads) {
+    if (!layer->heads_on) return HYMBA_OK;
     layer->heads_on = false;
     layer->mark->rope = hymba_rope{};
+    restamp(layer);
     return HYMBA_OK;
   }
   const hymba_layer_config &c = layer->cfg;
@@ -305,9 +324,13 @@ hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *
   if (!heads->norm && (heads->q_weight || heads->k_weight)) FAIL(HYMBA_ERR_INVALID_ARG, "a weight without the norm");
   if (!aligned16(heads->q_weight) || !aligned16(heads->k_weight))
     FAIL(HYMBA_ERR_INVALID_ARG, "weight pointer not 16-byte aligned");
+  const hymba_layer_heads &was = layer->heads;
+  const bool same = layer->heads_on && was.norm == heads->norm && was.eps == heads->eps &&
+                    was.q_weight == heads->q_weight && was.k_weight == heads->k_weight && same_rope(was.rope, heads->rope);
   layer->heads = *heads;
   layer->heads_on = true;
   layer->mark->rope = heads->rope;
+  if (!same) restamp(layer);
   return HYMBA_OK;
 }
 
@@ -315,7 +338,9 @@ hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hymba_linear
   g_msg[0] = 0;
   if (!layer) FAIL(HYMBA_ERR_INVALID_ARG, "null layer");
   if (!heads) {
+    if (!layer->linear_on) return HYMBA_OK;
     layer->linear_on = false;
+    restamp(layer);
     return HYMBA_OK;
   }
   const hymba_layer_config &c = layer->cfg;
@@ -326,23 +351,19 @@ hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hymba_linear
   if (2 * heads->d_state + c.n_heads > 360) FAIL(HYMBA_ERR_UNSUPPORTED, "2 * d_state + n_heads > 360");
   for (const void *p : {heads->w_x, (const void *)heads->b_dt, (const void *)heads->a_log, (const void *)heads->d_skip})
     if (!p || !aligned16(p)) FAIL(HYMBA_ERR_INVALID_ARG, "linear heads' weight pointer null or not 16-byte aligned");
+  const hymba_linear_heads &was = layer->linear;
+  const bool same = layer->linear_on && was.d_state == heads->d_state && was.w_x == heads->w_x &&
+                    was.b_dt == heads->b_dt && was.a_log == heads->a_log && was.d_skip == heads->d_skip;
   layer->linear = *heads;
   layer->linear_on = true;
+  if (!same) restamp(layer);
   return HYMBA_OK;
 }
 
 // A consumer reads keys at its producer's positions: both must rotate alike.
 static hymba_status check_rotation(const hymba_layer *layer) {
-  if (!layer->producer) return HYMBA_OK;
-  const hymba_rope &a = layer->mark->rope, &b = layer->producer->rope;
-  bool same = a.dim == b.dim;
-  if (same && a.dim > 0) {
-    same = a.layout == b.layout && a.scaling == b.scaling && a.base == b.base && a.attn_factor == b.attn_factor;
-    if (same && a.scaling != HYMBA_ROPE_SCALE_NONE) same = a.factor == b.factor;
-    if (same && a.scaling == HYMBA_ROPE_SCALE_WAVELENGTH)
-      same = a.orig_len == b.orig_len && a.low_turns == b.low_turns && a.high_turns == b.high_turns;
-  }
-  if (!same) FAIL(HYMBA_ERR_NOT_BOUND, "producer and consumer rotate their heads differently");
+  if (layer->producer && !same_rope(layer->mark->rope, layer->producer->rope))
+    FAIL(HYMBA_ERR_NOT_BOUND, "producer and consumer rotate their heads differently");
   return HYMBA_OK;
 }
 
@@ -902,10 +923,10 @@ static hymba_status prefill_run(hymba_layer *layer, int batch, const PrefillRun 
     a.window = c.window;
     a.is_global = c.is_global;
     if ((st = kv_cache_emit(a, c.dtype, stream)) != HYMBA_OK) return st;
-    kv_cache->owner = layer->mark->id;
+    kv_cache->owner = layer->mark->stamp;
   }
   if (!consumer) {
-    kv->owner = layer->mark->id;
+    kv->owner = layer->mark->stamp;
     kv->batch = batch;
     kv->rows = L;
   }
@@ -921,8 +942,8 @@ static hymba_status check_prefill_kv(const hymba_layer *layer, int batch, int L,
   if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v))
     FAIL(HYMBA_ERR_INVALID_ARG, "kv buffers null or misaligned");
   if (consumer) {
-    if (kv->owner != layer->producer->id)
-      FAIL(HYMBA_ERR_NOT_BOUND, "kv was not written by this consumer's producer");
+    if (kv->owner != layer->producer->stamp)
+      FAIL(HYMBA_ERR_NOT_BOUND, "kv was not written by this consumer's producer as its heads are set");
     if (kv->batch != batch || kv->rows != L)
       FAIL(HYMBA_ERR_NOT_BOUND, "producer K/V has batch %d rows %d, consumer needs %d x %d",
            kv->batch, kv->rows, batch, L);
@@ -990,8 +1011,8 @@ hymba_status hymba_layer_meta_precompute(hymba_layer *layer, const void *x_meta,
     FAIL(HYMBA_ERR_INVALID_ARG, "meta cache y/h/conv null or misaligned");
   hymba_kv_seq kv{};
   if (consumer) {
-    if (!producer_meta || producer_meta->owner != layer->producer->id)
-      FAIL(HYMBA_ERR_NOT_BOUND, "a consumer needs its producer's meta cache");
+    if (!producer_meta || producer_meta->owner != layer->producer->stamp)
+      FAIL(HYMBA_ERR_NOT_BOUND, "a consumer needs its producer's meta cache, as the producer's heads are set");
     kv.k = producer_meta->k;
     kv.v = producer_meta->v;
     kv.batch = 1;
@@ -1021,7 +1042,7 @@ hymba_status hymba_layer_meta_precompute(hymba_layer *layer, const void *x_meta,
   r.meta = true;
   st = prefill_run(layer, 1, r, &kv, nullptr, &ssm, workspace, lay, reinterpret_cast<cudaStream_t>(stream));
   if (st != HYMBA_OK) return st;
-  meta->owner = layer->mark->id;
+  meta->owner = layer->mark->stamp;
   return HYMBA_OK;
 }
 
@@ -1053,7 +1074,8 @@ hymba_status hymba_layer_prefill_cached(hymba_layer *layer, int batch, int n_tok
   if (st != HYMBA_OK) return st;
   const int L = c.n_meta + n_tokens;
   if (!x || !y || !aligned16(x) || !aligned16(y)) FAIL(HYMBA_ERR_INVALID_ARG, "x/y null or misaligned");
-  if (!meta || meta->owner != layer->mark->id) FAIL(HYMBA_ERR_NOT_BOUND, "meta cache not computed by this layer");
+  if (!meta || meta->owner != layer->mark->stamp)
+    FAIL(HYMBA_ERR_NOT_BOUND, "meta cache not computed by this layer as its heads are set");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     FAIL(HYMBA_ERR_INVALID_ARG, "workspace null or not 256-byte aligned");
   if (workspace_bytes < lay.total)
@@ -1154,10 +1176,10 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
   const long long need = c.is_global ? pos + 1 : (long long)c.n_meta + c.window;
   if (kv_cache->capacity < need)
     FAIL(HYMBA_ERR_INVALID_ARG, "kv_cache capacity %d < %lld", kv_cache->capacity, need);
-  if (consumer && kv_cache->owner != layer->producer->id)
-    FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache is not this consumer's producer's store");
-  if (!consumer && kv_cache->owner != 0 && kv_cache->owner != layer->mark->id)
-    FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache belongs to another layer");
+  if (consumer && kv_cache->owner != layer->producer->stamp)
+    FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache is not this consumer's producer's store as its heads are set");
+  if (!consumer && kv_cache->owner != 0 && kv_cache->owner != layer->mark->stamp)
+    FAIL(HYMBA_ERR_NOT_BOUND, "kv_cache belongs to another layer or to another setting of its heads");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     FAIL(HYMBA_ERR_INVALID_ARG, "workspace null or not 256-byte aligned");
   const DecodeLayout d = decode_layout(*layer, batch, pos);
@@ -1375,7 +1397,7 @@ static hymba_status decode_run(hymba_layer *layer, int batch, int64_t pos, const
     g.epi.nseg = 1;
     if ((st = gemm_decode(g, c.dtype, stream)) != HYMBA_OK) return st;
   }
-  if (!consumer) kv_cache->owner = layer->mark->id;
+  if (!consumer) kv_cache->owner = layer->mark->stamp;
   return HYMBA_OK;
 }
 

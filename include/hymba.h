@@ -130,7 +130,7 @@ typedef struct {
   void *v;
   int batch;
   int rows;
-  uint64_t owner;   /* set by the library; 0 = never written */
+  uint64_t owner;   /* set by the library: the handle and its head operators; 0 = never written */
 } hymba_kv_seq;
 
 /* Decode K/V store of a layer that owns K/V: k [batch, Hkv, capacity, d_qk],
@@ -521,7 +521,12 @@ typedef struct {
   const float *k_weight; /* [head_dim_qk] or NULL */
   hymba_rope rope;
 } hymba_layer_heads;
-/* NULL: back to the heads as projected.  Host only; no call on the handle may be running. */
+/* NULL: back to the heads as projected.  Host only; no call on the handle, nor on a consumer
+ * bound to it, may be running.  Meta caches, K/V sequences and decode stores hold what they were
+ * written under: after a change of this setting or of hymba_layer_set_linear_heads those of
+ * another setting are refused with NOT_BOUND (the same setting again keeps them, and without both
+ * operators the handle takes what it wrote without them).  hymba_ssm_cache carries no stamp: its
+ * size is the caller's to keep. */
 HYMBA_API hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_layer_heads *heads);
 
 /* The SSM branch with linear heads: hymba_linear_attention in place of the selective scan, the
@@ -543,8 +548,8 @@ typedef struct {
   const float *a_log;
   const float *d_skip;
 } hymba_linear_heads;
-/* NULL: back to the selective scan.  Host only; no call on the handle may be running.
- * Workspace sizes change: query them after the set. */
+/* NULL: back to the selective scan.  Host only, and what was stored before is refused, as for
+ * hymba_layer_set_heads.  Workspace sizes change: query them after the set. */
 HYMBA_API hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hymba_linear_heads *heads);
 
 /* ---- status and diagnostics -------------------------------------------- */

@@ -45,3 +45,62 @@ def test_a_consumer_outlives_its_producer():
     assert _stamp(_consumer_status, cons) == stamp
     for h in (cons, *others):
         hy.hymba_layer_destroy(h)
+
+
+def _meta_status(layer, owner: int) -> int:
+    """A prefill from a meta cache stamped `owner`, with a workspace that an accepted stamp finds too small."""
+    meta = hy.hymba_meta_cache(A, A, A, A, A, owner)
+    kv = hy.hymba_kv_seq(A, A, 0, 0, 0)
+    return _status(hy.hymba_layer_prefill_cached, layer, 1, 100, A, A, meta, kv, None, None, A, 256)
+
+
+def _store_status(layer, owner: int) -> int:
+    """A decode step on a store stamped `owner`, likewise."""
+    store = hy.hymba_kv_cache(A, A, 1, 200, owner)
+    return _status(hy.hymba_layer_decode_step, layer, 1, 150, A, A, store, hy.hymba_ssm_cache(A, A), A, 256)
+
+
+LINEAR = {n: A + 4096 * i for i, n in enumerate(("w_x", "b_dt", "a_log", "d_skip"))}
+SETTERS = {
+    "heads": (hy.hymba_layer_set_heads, lambda: hy.make_layer_heads(), lambda: hy.make_layer_heads(rope=hy.make_rope(64))),
+    "linear": (hy.hymba_layer_set_linear_heads, lambda: hy.make_linear_heads(LINEAR, 16),
+               lambda: hy.make_linear_heads(LINEAR, 128)),
+}
+
+
+@pytest.mark.parametrize("which", SETTERS)
+def test_data_of_another_head_setting_is_refused(which):
+    """A meta cache, K/V and decode store written before a head operator was set, changed or taken off hold
+    other keys, or a state of another size: NOT_BOUND.  Setting the same again keeps them, and the
+    plain heads accept what plain heads wrote."""
+    put, one, two = SETTERS[which]
+    lay, cons = _layer(), _layer()
+    hy.hymba_kv_share_bind(cons, lay)
+    uses = ((_meta_status, lay), (_store_status, lay), (_consumer_status, cons))
+
+    def stamps():
+        return {_stamp(f, h) for f, h in uses}
+
+    plain = stamps()
+    assert len(plain) == 1
+    put(lay, one())
+    first = stamps()
+    assert len(first) == 1 and first != plain
+    put(lay, one())
+    assert stamps() == first
+    put(lay, two())
+    second = stamps()
+    assert len(second) == 1 and second != first and second != plain
+    put(lay, one())
+    assert not stamps() & (first | second | plain)
+    with pytest.raises(hy.HymbaError):  # a refused setting changes nothing
+        now = stamps()
+        put(lay, hy.make_layer_heads(eps=-1.0) if which == "heads" else hy.make_linear_heads(LINEAR, 12))
+    assert stamps() == now
+    put(lay, None)
+    assert stamps() == plain
+    # the consumer's own setting concerns its own meta cache, not its producer's K/V
+    put(cons, two())
+    assert _stamp(_consumer_status, cons) in plain and _stamp(_meta_status, cons) not in plain
+    for h in (lay, cons):
+        hy.hymba_layer_destroy(h)
