@@ -833,8 +833,9 @@ hymba_status chunk_launch(const hymba_linear_attention &a, LinearSegments seg, c
   p.a = a;
   p.seg = seg;
   p.blocks = dv_blocks(a);
-  // A chain's waits are as long as a segment (about 50 cycles a row) when lengths differ.
-  const long long cycles = std::max<long long>(wait_limit_cycles(), seg.chain ? 500LL * seg.rows : 0);
+  // When lengths differ, all segments of a long chain may run beside each other: the last one then
+  // waits for all before it, at 50 (dk <= 64) to 90 cycles a row, and so do the other roles of its CTA.
+  const long long cycles = std::max<long long>(wait_limit_cycles(), seg.chain ? 500LL * seg.rows * seg.n : 0);
   p.wlim = cycles > 0x7fffffffLL ? 0x7fffffffu : (unsigned)cycles;
   const long long ctas = (long long)a.batch * a.n_heads * p.blocks;
   if (ctas * seg.n > 0x7fffffffLL) {

@@ -558,8 +558,9 @@ HYMBA_API hymba_status hymba_layer_set_linear_heads(hymba_layer *layer, const hy
  * error word (e.g. a bounded wait that timed out) and clears the word. */
 HYMBA_API hymba_status hymba_stream_status(hymba_stream_t stream);
 /* Bounded device waits.  Every wait of the tensor-core kernels on an mbarrier (a TMA
- * copy, an MMA, a pipeline stage), and the linear attention's wait for the segment of rows
- * before its own, gives up after a limit in SM clock cycles, records a
+ * copy, an MMA, a pipeline stage), and the linear attention's wait for the segments of rows
+ * before its own (for which it grants 500 cycles for each row of the call, if that is more),
+ * gives up after a limit in SM clock cycles, records a
  * timeout in the library's device error word, drains what its CTA has in flight, releases
  * its tensor memory and returns; hymba_stream_status() then reports HYMBA_ERR_TIMEOUT.
  * This sets the limit for launches issued from now on: `cycles` >= 1e5 (smaller values

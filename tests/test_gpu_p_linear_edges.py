@@ -5,6 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+import hybrid_attention_ssm_head_b200 as hy
 from tests import _operators as P
 from tests.test_gpu_n_linear import DT, check, inputs, on_gpu, prefill
 
@@ -45,3 +46,23 @@ def test_a_non_finite_value_reaches_no_row_before_its_own(name, t, dtype, B, L, 
             assert bool(o[0, at:, 0].isnan().all())
         else:
             assert torch.equal(o[0, at + 1:], clean[0, at + 1:])
+
+
+def test_a_long_chain_beside_short_sequences_keeps_a_low_wait_limit():
+    """Six heads of 65536 rows, 180 of at most one: the segments of a chain (19 of 3456 rows) all start at
+    once and the last one waits for the others, 18 * 3456 rows at 50 cycles, 3.1e6.  With the lowest
+    limit, 1e5 cycles, the call grants its chains 500 cycles for each of their rows, 3.3e7."""
+    B, L, H, dk, dv = 31, 65536, 6, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    lengths = torch.tensor([L] + [1, 0] * 15, dtype=torch.int32, device="cuda")
+    dev = dict(q=n(B, L, 1, dk), k=n(B, L, 1, dk), v=n(B, L, H, dv), lengths=lengths,
+               log_decay=torch.full((1, 1, H), -0.01, device="cuda").expand(B, L, H))
+    want = prefill(dev, B, L, H, dv, dk)
+    try:
+        assert hy.hymba_set_wait_limit(1) == 100000
+        o, S = prefill(dev, B, L, H, dv, dk)
+    finally:
+        hy.hymba_set_wait_limit(0)
+    assert torch.equal(o, want[0]) and torch.equal(S, want[1])
+    assert bool(torch.isfinite(S[0]).all()) and bool((S[0] != 0).any())
