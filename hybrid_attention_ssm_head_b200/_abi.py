@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhymba.so")
@@ -375,7 +376,22 @@ def hymba_layer_set_linear_heads(layer: int, heads: hymba_linear_heads | None) -
           "hymba_layer_set_linear_heads")
 
 
+def _launchable(args, what: str, workspace=None) -> None:
+    """A description made from tensors runs on their GPU, which has to be the current device.  (One
+    filled in by hand carries no device: its addresses are the caller's.)"""
+    dev = getattr(args, "device", None)
+    if dev is None:
+        return
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: the tensors are on {dev}, not on a GPU")
+    if dev.index != sys.modules["torch"].cuda.current_device():
+        raise ValueError(f"{what}: the tensors are on {dev}, which is not the current device")
+    if getattr(workspace, "device", dev) != dev:
+        raise ValueError(f"{what}: the workspace is on {workspace.device}, the tensors on {dev}")
+
+
 def hymba_qk_norm_rope(args: hymba_qk_norm_rope_args, stream=None) -> None:
+    _launchable(args, "hymba_qk_norm_rope")
     check(lib().hymba_qk_norm_rope(C.byref(args), _stream(stream)), "hymba_qk_norm_rope")
 
 
@@ -387,11 +403,13 @@ def hymba_linear_attention_workspace(args: hymba_linear_attention) -> int:
 
 def hymba_linear_attention_prefill(args: hymba_linear_attention, workspace, workspace_bytes: int,
                                    stream=None) -> None:
+    _launchable(args, "hymba_linear_attention_prefill", workspace)
     check(lib().hymba_linear_attention_prefill(C.byref(args), _ptr(workspace), workspace_bytes, _stream(stream)),
           "hymba_linear_attention_prefill")
 
 
 def hymba_linear_attention_decode_step(args: hymba_linear_attention, stream=None) -> None:
+    _launchable(args, "hymba_linear_attention_decode_step")
     check(lib().hymba_linear_attention_decode_step(C.byref(args), _stream(stream)),
           "hymba_linear_attention_decode_step")
 
@@ -480,6 +498,14 @@ def _dtype_of(t) -> int:
     return HYMBA_BF16 if name == "torch.bfloat16" else HYMBA_F32
 
 
+def _one_device(**tensors):
+    """The device all of them are on."""
+    on = {n: t.device for n, t in tensors.items() if t is not None}
+    if len(set(on.values())) > 1:
+        raise ValueError("tensors on different devices: " + ", ".join(f"{n} on {d}" for n, d in on.items()))
+    return next(iter(on.values()))
+
+
 def _rows(name: str, t, shape, dtype: str) -> list[int]:
     """[pointer, batch, row and head stride] of a [batch, rows, heads(, dim)] tensor; checks what
     the library cannot see: shape, dtype and a contiguous last dimension."""
@@ -514,8 +540,8 @@ def make_qk_norm_rope(q, k, q_out=None, k_out=None, norm: bool = True, eps: floa
                       k_weight=None, rope: hymba_rope | None = None, pos0: int = 0,
                       positions=None) -> hymba_qk_norm_rope_args:
     """q [batch, rows, heads, dim], k [batch, rows, kv_heads, dim] or None: device tensors of any
-    strides with a contiguous head; q_out, k_out likewise (None: in place).  The description holds
-    addresses only: the tensors must outlive its use."""
+    strides with a contiguous head; q_out, k_out likewise (None: in place).  All on one device.  The
+    description holds addresses only: the tensors must outlive its use."""
     some = q if q is not None else k
     B, R, _, d = some.shape
     a = hymba_qk_norm_rope_args(dtype=_dtype_of(some), batch=B, n_rows=R, head_dim=d, norm=int(norm), eps=eps,
@@ -530,6 +556,7 @@ def make_qk_norm_rope(q, k, q_out=None, k_out=None, norm: bool = True, eps: floa
                                          x.shape[2]))
     if rope is not None:
         a.rope = rope
+    a.device = _one_device(q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, positions=positions)
     a.positions = _dense("positions", positions, (B, R), "torch.int64")
     return a
 
@@ -539,8 +566,8 @@ def make_linear_attention(q, k, v, o, log_decay=None, in_scale=None, skip=None, 
     """q, k [batch, rows, qk_heads, dk], v, o, gate [batch, rows, heads, dv]: device tensors of any
     strides with a contiguous head; log_decay, in_scale [batch, rows, heads] fp32 of any strides
     (expand() repeats a value); skip [heads, dv]; state_in [batch, heads, dv, dk] dense per sequence
-    (expand() over the batch repeats one); state_out likewise, dense; lengths [batch] int32.  The
-    description holds addresses only: the tensors must outlive its use."""
+    (expand() over the batch repeats one); state_out likewise, dense; lengths [batch] int32.  All on one
+    device.  The description holds addresses only: the tensors must outlive its use."""
     B, L, K, dk = q.shape
     H, dv = v.shape[2], v.shape[3]
     dt = str(q.dtype)
@@ -557,6 +584,8 @@ def make_linear_attention(q, k, v, o, log_decay=None, in_scale=None, skip=None, 
             setattr(a, stride + "_batch", sb)
             setattr(a, stride + "_row", sr)
             setattr(a, stride + "_head", sh)
+    a.device = _one_device(q=q, k=k, v=v, o=o, log_decay=log_decay, in_scale=in_scale, skip=skip, gate=gate,
+                           state_in=state_in, state_out=state_out, lengths=lengths)
     a.skip = _dense("skip", skip, (H, dv), "torch.float32")
     if state_in is not None:
         if tuple(state_in.shape) != (B, H, dv, dk):

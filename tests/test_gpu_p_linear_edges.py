@@ -66,3 +66,19 @@ def test_a_long_chain_beside_short_sequences_keeps_a_low_wait_limit():
         hy.hymba_set_wait_limit(0)
     assert torch.equal(o, want[0]) and torch.equal(S, want[1])
     assert bool(torch.isfinite(S[0]).all()) and bool((S[0] != 0).any())
+
+
+def test_another_device_or_a_host_workspace_is_refused():
+    """Before any launch: a description of tensors of another GPU than the current one (one index further
+    here), and a workspace on the host."""
+    x = on_gpu(inputs("bf16", 1, 300, 2, 1, 16, 16))
+    o, S = torch.zeros(1, 300, 2, 16, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 2, 16, 16, device="cuda")
+    args = hy.make_linear_attention(o=o, state_out=S, **x)
+    n = hy.hymba_linear_attention_workspace(args)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        hy.hymba_linear_attention_prefill(args, torch.empty(n + 256, dtype=torch.uint8), n)
+    assert args.device == o.device
+    args.device = torch.device("cuda", o.device.index + 1)
+    with pytest.raises(ValueError, match="not the current device"):
+        hy.hymba_linear_attention_prefill(args, torch.empty(n + 256, dtype=torch.uint8, device="cuda"), n)
+    assert not bool(o.any())

@@ -1,7 +1,8 @@
-"""Handles and stored data of the layer's head operators, checked before any launch (CPU only)."""
+"""What the layer's head operators and the operators' descriptions check before any launch (CPU only)."""
 from __future__ import annotations
 
 import pytest
+import torch
 
 import hybrid_attention_ssm_head_b200 as hy
 from tests.test_operators_host import A, _layer
@@ -104,3 +105,35 @@ def test_data_of_another_head_setting_is_refused(which):
     assert _stamp(_consumer_status, cons) in plain and _stamp(_meta_status, cons) not in plain
     for h in (lay, cons):
         hy.hymba_layer_destroy(h)
+
+
+def _linear_tensors(B=2, L=3, nh=2, dk=8, dv=8):
+    t = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    return dict(q=t(B, L, 1, dk), k=t(B, L, 1, dk), v=t(B, L, nh, dv), o=t(B, L, nh, dv))
+
+
+def test_host_tensors_are_not_launched_on():
+    """A kernel that got a host address would fault."""
+    x = _linear_tensors()
+    one = {n: v[:, :1] for n, v in x.items()}
+    state = torch.zeros(2, 2, 8, 8)
+    calls = ((hy.hymba_linear_attention_prefill, hy.make_linear_attention(**x), A, 1 << 30),
+             (hy.hymba_linear_attention_decode_step, hy.make_linear_attention(**one, state_out=state)),
+             (hy.hymba_qk_norm_rope, hy.make_qk_norm_rope(x["q"], x["k"])))
+    for call, *args in calls:
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call(*args)
+
+
+def test_tensors_of_one_description_are_on_one_device():
+    x = _linear_tensors()
+    other = dict(lengths=torch.zeros(2, dtype=torch.int32, device="meta"), skip=torch.zeros(2, 8, device="meta"),
+                 state_in=torch.zeros(2, 2, 8, 8, device="meta"), log_decay=torch.zeros(2, 3, 2, device="meta"),
+                 v=x["v"].to("meta"), gate=x["v"].to("meta"))
+    for n, t in other.items():
+        with pytest.raises(ValueError, match="different devices"):
+            hy.make_linear_attention(**{**x, n: t})
+    for kw in (dict(q_weight=torch.zeros(8, device="meta")), dict(k_out=x["k"].to("meta")),
+               dict(positions=torch.zeros(2, 3, dtype=torch.int64, device="meta"))):
+        with pytest.raises(ValueError, match="different devices"):
+            hy.make_qk_norm_rope(x["q"], x["k"], **kw)
