@@ -597,11 +597,32 @@ def make_linear_attention(q, k, v, o, log_decay=None, in_scale=None, skip=None, 
     return a
 
 
+def _weight(name: str, t, dtype: str | None = None, shape=None) -> int | None:
+    """Address of a weight.  A tensor has to be contiguous and, where given, of this dtype and shape."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_contiguous():
+        raise ValueError(f"weight {name} must be contiguous")
+    if (dtype and str(t.dtype) != dtype) or (shape and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"weight {name}: {tuple(t.shape)} {t.dtype}, expected {shape or 'any shape'} {dtype or ''}")
+    return t.data_ptr()
+
+
 def make_layer_heads(norm: bool = True, eps: float = 1e-6, q_weight=None, k_weight=None,
                      rope: hymba_rope | None = None) -> hymba_layer_heads:
-    return hymba_layer_heads(int(norm), eps, _ptr(q_weight), _ptr(k_weight), rope if rope is not None else hymba_rope())
+    """q_weight, k_weight [head_dim_qk] fp32 device tensors or None."""
+    return hymba_layer_heads(int(norm), eps, _weight("q_weight", q_weight, "torch.float32"),
+                             _weight("k_weight", k_weight, "torch.float32"), rope if rope is not None else hymba_rope())
 
 
 def make_linear_heads(w: dict, d_state: int) -> hymba_linear_heads:
-    """From device tensors w_x [2 * d_state + n_heads, d_inner], b_dt and a_log [n_heads], d_skip [d_inner]."""
-    return hymba_linear_heads(d_state, *[_ptr(w[n]) for n in ("w_x", "b_dt", "a_log", "d_skip")])
+    """From device tensors w_x [2 * d_state + n_heads, d_inner] of the layer's dtype, and fp32 b_dt and
+    a_log [n_heads], d_skip [d_inner]."""
+    b, x = w["b_dt"], w["w_x"]
+    heads = tuple(b.shape) if hasattr(b, "shape") else None
+    wide = hasattr(x, "shape")
+    if wide and (x.ndim != 2 or (heads and x.shape[0] != 2 * d_state + heads[0])):
+        raise ValueError(f"weight w_x: {tuple(x.shape)}, expected (2 * {d_state} + n_heads, d_inner)")
+    return hymba_linear_heads(d_state, _weight("w_x", x), _weight("b_dt", b, "torch.float32"),
+                              _weight("a_log", w["a_log"], "torch.float32", heads),
+                              _weight("d_skip", w["d_skip"], "torch.float32", (x.shape[1],) if wide else None))

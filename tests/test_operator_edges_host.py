@@ -137,3 +137,22 @@ def test_tensors_of_one_description_are_on_one_device():
                dict(positions=torch.zeros(2, 3, dtype=torch.int64, device="meta"))):
         with pytest.raises(ValueError, match="different devices"):
             hy.make_qk_norm_rope(x["q"], x["k"], **kw)
+
+
+def test_head_weights_are_checked_for_what_the_library_cannot_see():
+    nh, E, n = 4, 32, 8
+    good = dict(w_x=torch.zeros(2 * n + nh, E, dtype=torch.bfloat16), b_dt=torch.zeros(nh), a_log=torch.zeros(nh),
+                d_skip=torch.zeros(E))
+    lh = hy.make_linear_heads(good, n)
+    assert lh.w_x == good["w_x"].data_ptr() and lh.d_state == n
+    for bad in (dict(w_x=torch.zeros(E, 2 * n + nh).t()), dict(w_x=torch.zeros(2 * n, E)), dict(w_x=torch.zeros(E)),
+                dict(b_dt=torch.zeros(nh, dtype=torch.bfloat16)), dict(a_log=torch.zeros(nh + 1)),
+                dict(a_log=torch.zeros(2 * nh)[::2]), dict(d_skip=torch.zeros(E, dtype=torch.bfloat16)),
+                dict(d_skip=torch.zeros(nh))):
+        with pytest.raises(ValueError):
+            hy.make_linear_heads({**good, **bad}, n)
+    w = torch.zeros(64)
+    assert hy.make_layer_heads(q_weight=w, k_weight=A).q_weight == w.data_ptr()
+    for bad in (w.bfloat16(), torch.zeros(128)[::2]):
+        with pytest.raises(ValueError):
+            hy.make_layer_heads(k_weight=bad)
