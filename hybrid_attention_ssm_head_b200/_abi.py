@@ -85,13 +85,18 @@ class hymba_head_rows(C.Structure):
                 ("n_heads", C.c_int)]
 
 
-class hymba_qk_norm_rope_args(C.Structure):
+class _Description(C.Structure):
+    device = None         # of the tensors a maker took the addresses of
+    check_device = False  # whether a call has to look at it
+
+
+class hymba_qk_norm_rope_args(_Description):
     _fields_ = [("dtype", C.c_int), ("batch", C.c_int), ("n_rows", C.c_int), ("head_dim", C.c_int),
                 ("q", hymba_head_rows), ("k", hymba_head_rows), ("norm", C.c_int), ("eps", C.c_float),
                 ("rope", hymba_rope), ("pos0", C.c_int64), ("positions", C.c_void_p)]
 
 
-class hymba_linear_attention(C.Structure):
+class hymba_linear_attention(_Description):
     _fields_ = ([(n, C.c_int) for n in ("dtype", "batch", "n_rows", "n_heads", "n_qk_heads", "dk", "dv")] +
                 [("scale", C.c_float)] +
                 [f for n, s in (("q", "q"), ("k", "k"), ("v", "v"), ("o", "o"), ("gate", "gate"),
@@ -379,19 +384,19 @@ def hymba_layer_set_linear_heads(layer: int, heads: hymba_linear_heads | None) -
 def _launchable(args, what: str, workspace=None) -> None:
     """A description made from tensors runs on their GPU, which has to be the current device.  (One
     filled in by hand carries no device: its addresses are the caller's.)"""
-    dev = getattr(args, "device", None)
-    if dev is None:
-        return
-    if dev.type != "cuda":
+    dev = args.device
+    if dev is not None and dev.type != "cuda":
         raise ValueError(f"{what}: the tensors are on {dev}, not on a GPU")
-    if dev.index != sys.modules["torch"].cuda.current_device():
+    if dev is not None and dev.index != sys.modules["torch"].cuda.current_device():
         raise ValueError(f"{what}: the tensors are on {dev}, which is not the current device")
-    if getattr(workspace, "device", dev) != dev:
-        raise ValueError(f"{what}: the workspace is on {workspace.device}, the tensors on {dev}")
+    on = getattr(workspace, "device", dev)
+    if on is not None and (on.type != "cuda" or (dev is not None and on != dev)):
+        raise ValueError(f"{what}: the workspace is on {on}, the tensors on {dev}")
 
 
 def hymba_qk_norm_rope(args: hymba_qk_norm_rope_args, stream=None) -> None:
-    _launchable(args, "hymba_qk_norm_rope")
+    if args.check_device:
+        _launchable(args, "hymba_qk_norm_rope")
     check(lib().hymba_qk_norm_rope(C.byref(args), _stream(stream)), "hymba_qk_norm_rope")
 
 
@@ -403,13 +408,15 @@ def hymba_linear_attention_workspace(args: hymba_linear_attention) -> int:
 
 def hymba_linear_attention_prefill(args: hymba_linear_attention, workspace, workspace_bytes: int,
                                    stream=None) -> None:
-    _launchable(args, "hymba_linear_attention_prefill", workspace)
+    if args.check_device or not getattr(workspace, "is_cuda", True):
+        _launchable(args, "hymba_linear_attention_prefill", workspace)
     check(lib().hymba_linear_attention_prefill(C.byref(args), _ptr(workspace), workspace_bytes, _stream(stream)),
           "hymba_linear_attention_prefill")
 
 
 def hymba_linear_attention_decode_step(args: hymba_linear_attention, stream=None) -> None:
-    _launchable(args, "hymba_linear_attention_decode_step")
+    if args.check_device:
+        _launchable(args, "hymba_linear_attention_decode_step")
     check(lib().hymba_linear_attention_decode_step(C.byref(args), _stream(stream)),
           "hymba_linear_attention_decode_step")
 
@@ -498,12 +505,13 @@ def _dtype_of(t) -> int:
     return HYMBA_BF16 if name == "torch.bfloat16" else HYMBA_F32
 
 
-def _one_device(**tensors):
-    """The device all of them are on."""
+def _set_device(args: _Description, **tensors) -> None:
+    """The device all of them are on.  It is looked at again at each call, unless there is but one GPU."""
     on = {n: t.device for n, t in tensors.items() if t is not None}
     if len(set(on.values())) > 1:
         raise ValueError("tensors on different devices: " + ", ".join(f"{n} on {d}" for n, d in on.items()))
-    return next(iter(on.values()))
+    args.device = next(iter(on.values()))
+    args.check_device = args.device.type != "cuda" or sys.modules["torch"].cuda.device_count() > 1
 
 
 def _rows(name: str, t, shape, dtype: str) -> list[int]:
@@ -556,7 +564,7 @@ def make_qk_norm_rope(q, k, q_out=None, k_out=None, norm: bool = True, eps: floa
                                          x.shape[2]))
     if rope is not None:
         a.rope = rope
-    a.device = _one_device(q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, positions=positions)
+    _set_device(a, q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, positions=positions)
     a.positions = _dense("positions", positions, (B, R), "torch.int64")
     return a
 
@@ -584,8 +592,8 @@ def make_linear_attention(q, k, v, o, log_decay=None, in_scale=None, skip=None, 
             setattr(a, stride + "_batch", sb)
             setattr(a, stride + "_row", sr)
             setattr(a, stride + "_head", sh)
-    a.device = _one_device(q=q, k=k, v=v, o=o, log_decay=log_decay, in_scale=in_scale, skip=skip, gate=gate,
-                           state_in=state_in, state_out=state_out, lengths=lengths)
+    _set_device(a, q=q, k=k, v=v, o=o, log_decay=log_decay, in_scale=in_scale, skip=skip, gate=gate,
+                state_in=state_in, state_out=state_out, lengths=lengths)
     a.skip = _dense("skip", skip, (H, dv), "torch.float32")
     if state_in is not None:
         if tuple(state_in.shape) != (B, H, dv, dk):

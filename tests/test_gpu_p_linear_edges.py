@@ -78,7 +78,7 @@ def test_another_device_or_a_host_workspace_is_refused():
     with pytest.raises(ValueError, match="workspace is on cpu"):
         hy.hymba_linear_attention_prefill(args, torch.empty(n + 256, dtype=torch.uint8), n)
     assert args.device == o.device
-    args.device = torch.device("cuda", o.device.index + 1)
+    args.device, args.check_device = torch.device("cuda", o.device.index + 1), True
     with pytest.raises(ValueError, match="not the current device"):
         hy.hymba_linear_attention_prefill(args, torch.empty(n + 256, dtype=torch.uint8, device="cuda"), n)
     assert not bool(o.any())
