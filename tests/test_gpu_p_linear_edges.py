@@ -82,3 +82,67 @@ def test_another_device_or_a_host_workspace_is_refused():
     with pytest.raises(ValueError, match="not the current device"):
         hy.hymba_linear_attention_prefill(args, torch.empty(n + 256, dtype=torch.uint8, device="cuda"), n)
     assert not bool(o.any())
+
+
+@pytest.mark.parametrize("dtype,L", [("bf16", 150), ("bf16", 9), ("f32", 60)])
+@pytest.mark.parametrize("order", [(2, 0, 1), (1, 0, 2), (1, 2, 0), (2, 1, 0)])
+def test_any_order_of_sequences_rows_and_heads(dtype, L, order):
+    """q, k, v, gate, o, log_decay and in_scale stored with their dimensions in another order give the bits
+    of the dense call: a row's stride below its sequence's or its head's, or above both."""
+    B, nh, K, dk, dv = 3, 4, 2, 40, 72
+    x = inputs(dtype, B, L, nh, K, dk, dv, lengths=[L, 3, L - 1])
+    dev = on_gpu(x)
+    want = prefill(dev, B, L, nh, dv, dk)
+    back = [order.index(i) for i in range(3)]
+
+    def moved(t):
+        rest = list(range(3, t.ndim))
+        return t.permute(*order, *rest).contiguous().permute(*back, *rest)
+
+    other = {n: moved(t) if n in ("q", "k", "v", "gate", "log_decay", "in_scale") else t for n, t in dev.items()}
+    o = moved(torch.full((B, L, nh, dv), 7.0, dtype=DT[dtype], device="cuda"))
+    got = prefill(other, B, L, nh, dv, dk, o=o)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("far", ["row", "batch", "head"])
+def test_offsets_beyond_32_bits(dtype, far):
+    """Rows, sequences or heads 2^27 .. 2^32 elements apart in one buffer (8.6 GB and more): the dense call's
+    bits, from the whole sequences, a single token and the head norm/rotation."""
+    B, L, nh, K, dk, dv = 2, 40, 2, 1, 64, 64
+    x = inputs(dtype, B, L, nh, K, dk, dv, epilogue=True, start=True)
+    dev = on_gpu(x)
+    extent = {"row": L, "batch": B, "head": nh}[far]
+    step = (1 << 32) // (extent - 1) // 8 * 8 + 8
+    buf = torch.empty((extent - 1) * step + B * L * nh * dv * 8 + 65536, dtype=DT[dtype], device="cuda")
+    at = 0
+
+    def place(t):
+        nonlocal at
+        b, r, h, d = t.shape
+        st = {"row": (h * d * 5, step, d * 5), "batch": (step, h * d, d), "head": (r * d, d, step)}[far]
+        view = buf.as_strided((b, r, h, d), (*st, 1), at)
+        at += sum((n - 1) * s for n, s, f in zip((b, r, h), st, ("batch", "row", "head")) if f != far) + d
+        at = (at + 63) // 64 * 64
+        view.copy_(t)
+        return view
+
+    assert (extent - 1) * step >= 1 << 32
+    apart = {n: place(t) if n in ("q", "k", "v", "gate") else t for n, t in dev.items()}
+    o = place(torch.full((B, L, nh, dv), 7.0, dtype=DT[dtype], device="cuda"))
+    assert at <= B * L * nh * dv * 8 + 65536
+    want, got = prefill(dev, B, L, nh, dv, dk), prefill(apart, B, L, nh, dv, dk, o=o)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for n in ("q", "k", "v", "gate"):
+        assert torch.equal(apart[n], dev[n]), n
+    last = lambda y: {n: t[:, -1:] if torch.is_tensor(t) and n not in ("skip", "state_in") else t for n, t in y.items()}  # noqa: E731
+    for src, out in ((dev, want[0]), (apart, o)):
+        state = torch.empty(B, nh, dv, dk, device="cuda")
+        hy.hymba_linear_attention_decode_step(hy.make_linear_attention(o=out[:, -1:], state_out=state, **last(src)),
+                                              torch.cuda.current_stream())
+    qk = [hy.make_qk_norm_rope(y["v"], y["q"], y["v"], y["q"], rope=hy.make_rope(64, "halves")) for y in (dev, apart)]
+    for a in qk:
+        hy.hymba_qk_norm_rope(a, torch.cuda.current_stream())
+    hy.hymba_stream_status(torch.cuda.current_stream())
+    assert torch.equal(o, want[0]) and torch.equal(apart["v"], dev["v"]) and torch.equal(apart["q"], dev["q"])
