@@ -76,13 +76,15 @@ enum Partner {
 // for all heads of the unit.  32 / lanes heads are in flight per load, kAhead loads ahead of
 // the arithmetic.
 //
-// Bound by instructions more than by HBM: per element a share of the conversions, of the
-// norm's sum over the head's lanes and of the rotation.  With a head's halves in lanes of
-// their own the rotation took eight shuffles per eight elements (109 us at 8 x 4224 rows of
-// 30 heads of 64); a lane that holds both elements of its pairs needs none (62 us), and with
-// sixteen elements a lane the sums' shuffles are a third (57 us, 4.6 TB/s).  Not kept: loads two
-// or three ahead (59, 64 us), the first loads ahead of the angles (66 us with eight elements),
-// registers cut for more warps (61 us).
+// Bound by the latency inside a warp: it lives for one row, and angles, loads, sums and turns follow
+// one another.  8 x 4224 rows of 30 heads of 64, halves, under ncu: 18 warps an SM (96 registers a
+// thread) with an instruction every 8.1 cycles each, of which 2.0 are fixed waits between dependent
+// instructions, 1.6 loads, 1.5 shuffles and shared memory; instructions issue in 56 % of the cycles,
+// DRAM moves 3.6 TB/s.  What helped was fewer of them in a row: with a head's halves in lanes
+// of their own the rotation took eight shuffles per eight elements (109 us); a lane that holds
+// both elements of its pairs needs none (62 us), and with sixteen elements a lane the sums' shuffles
+// are a third (56 us, 4.6 TB/s).  Not kept: loads two or three ahead (59, 64 us), the first loads
+// ahead of the angles (66 us with eight elements), registers cut for more warps (61 us).
 template <typename T, int PARTNER, int N, int AHEAD>
 __global__ void __launch_bounds__(32 * kHeadWarps)
     qk_norm_rope_kernel(const __grid_constant__ HeadsParams p) {

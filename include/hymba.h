@@ -370,11 +370,12 @@ HYMBA_API hymba_status hymba_block_decode_step(hymba_layer *layer, const hymba_b
 
 /* The operators below work on rows of heads: a [batch, n_rows, n_heads, dim] grid given by a
  * pointer and the element strides between sequences, rows and heads (a head's dim elements
- * are contiguous).  Unlike the layer calls' densely packed tensors, any strides are taken
- * that keep every head 16-byte aligned, so that heads can be read and written where another
- * step left them: side by side in a fused projection, or in the slots of a K/V store.  The
- * written elements of one grid must not overlap each other (checked), nor any input other
- * than as stated (the caller's duty).  A stride over an extent of one is not looked at. */
+ * are contiguous).  Unlike the layer calls' densely packed tensors, any strides (below 2^38
+ * elements) are taken that keep every head 16-byte aligned, so that heads can be read and
+ * written where another step left them: side by side in a fused projection, or in the slots of a
+ * K/V store.  The written elements of one grid must not overlap each other (checked), nor any
+ * input other than as stated (the caller's duty).  A stride over an extent of one is not looked
+ * at. */
 
 /* Position rotation of a head's first `dim` elements: pair i of dim / 2 is turned by the
  * angle p * f_i at position p (§2.5 changes "the RoPE base" for longer contexts), and scaled:
@@ -449,7 +450,8 @@ HYMBA_API hymba_status hymba_qk_norm_rope(const hymba_qk_norm_rope_args *args, h
  *              for each head), or NULL (no decay).  g <= 0; below -110, -infinity included,
  *              the state is forgotten (exp(g) is 0 in fp32), as at the start of a document.
  *              Between -87 and -110 exp(g) is below fp32's normal range: what it leaves of the
- *              state keeps few bits or none.
+ *              state keeps few bits or none.  A non-finite state is not forgotten (0 times
+ *              infinity is NaN).
  *   in_scale   s, likewise, or NULL (1)
  *   skip       [n_heads, dv] fp32 or NULL (0)
  *   state_in   S_0, each sequence's [n_heads, dv, dk] dense, state_in_batch floats apart (0: one
@@ -459,9 +461,10 @@ HYMBA_API hymba_status hymba_qk_norm_rope(const hymba_qk_norm_rope_args *args, h
  *   lengths    [batch] int32 (device) or NULL: rows from lengths[b] on (clamped to 0..n_rows)
  *              do not change the state of sequence b, and their o is left as it was, whatever
  *              their inputs hold, infinities and NaN included.
- * dk a multiple of 8 up to 128, dv a multiple of 8 up to 256.  q, k, v, o, gate: strides > 0
- * where the extent is above one.  o must not overlap any input.
- * A non-finite value in a row reaches that row's output and the rows after it; in
+ * dk a multiple of 8 up to 128, dv a multiple of 8 up to 256; at most 65535 sequences and heads and
+ * 2^30 rows.  q, k, v, o, gate: strides > 0 where the extent is above one.  o must not overlap any
+ * input.
+ * A non-finite value in a row reaches that row's output and the rows after it, none before it; in
  * hymba_linear_attention_prefill with bf16 storage a non-finite v_t may also reach the
  * outputs of the up to 127 rows before row t, which are computed together with it. */
 typedef struct {
@@ -540,7 +543,9 @@ HYMBA_API hymba_status hymba_layer_set_heads(hymba_layer *layer, const hymba_lay
  * regions xdbl and delta hold other intermediates.
  *   w_x     [2 * d_state + n_heads, d_inner] dtype; rows: B, C, then one delta per head
  *   b_dt, a_log  [n_heads];  d_skip [d_inner] D
- * d_state a multiple of 8 up to 128; head_dim_v a multiple of 8.  Pointers kept as above. */
+ * d_state a multiple of 8 up to 128, 2 * d_state + n_heads at most 360 (the decode step keeps a
+ * block of w_x's columns in shared memory); head_dim_v a multiple of 8 up to 256.  Pointers kept
+ * as above. */
 typedef struct {
   int d_state;
   const void *w_x;
